@@ -1,0 +1,359 @@
+// Page tables, slot maps and the write of new tokens into a paged K/V cache.
+//
+// A paged cache keeps K and V as [num_pages, Hk, page, d]; a request's own tokens lie in the pages
+// its table row lists, in order.  Free pages wait in a ring: free = {head, avail} says that
+// ring[(head + i) mod N], i < avail, are free (N = num_pages = the ring's length).
+//
+// page_tables_kernel.  One step moves every request from lens[b] to new_lens[b] tokens.  With
+// have = ceil(lens / page), want = ceil(new_lens / page), grow = max(0, want - have) and the
+// inclusive sum G_b of grow over requests, request b is served iff grow_b = 0 or G_b <= avail (so a
+// pool that runs dry refuses whole requests, in order, never half of one), and takes ring entries
+// G_b - grow_b .. G_b - 1 behind head.  A shrinking request's pages go to the ring's end in request
+// order.  Token t of the packed new tokens belongs to the request whose range of the exclusive sum
+// of new tokens holds it, found by a binary search in shared memory.  All integer work on a few KB:
+// what bounds it is latency (the lengths' load, a block scan, the dependent page-id load), so it is
+// ONE launch: a cluster of up to 8 CTAs, each of which scans all requests for itself (one load and
+// a scan are cheaper than a second launch or a grid-wide exchange) and then handles its share of
+// the requests' pages and of the tokens.  The cluster barrier between reading lens / free and
+// writing lens_out / free_out lets the caller pass the same arrays (a state advanced in place).
+//
+// paged_append_kernel.  A copy bound by HBM: one 16-byte chunk of K and of V per thread and step,
+// neighbouring threads on neighbouring chunks of a head's row (256 B at d = 128 bf16), so reads
+// and writes are whole 32-byte sectors whatever the slots' order.
+#include <cooperative_groups.h>
+
+#include "bsa_common.cuh"
+
+namespace bsa {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kPtThreads = 1024;
+constexpr int kPtMaxB = 8192;      // requests of a step (shared memory: four ints each)
+constexpr int kPtCluster = 8;      // portable cluster size
+// Up to this many requests + new tokens one CTA does it all: above, its 1024 threads would take
+// more than a few rounds.
+constexpr int kPtOneCta = 4096;
+
+struct PageTablesParams {
+  int B, page_shift, ld, N, max_tokens, pos_offset;
+  const int *lens, *new_lens;
+  int *table, *ring;
+  const int* free_in;
+  int *lens_out, *free_out, *cu_new, *slots, *positions, *status;
+};
+
+struct Sum3 {
+  long long grow, drop, add;
+};
+__device__ __forceinline__ Sum3 operator+(const Sum3& a, const Sum3& b) {
+  return {a.grow + b.grow, a.drop + b.drop, a.add + b.add};
+}
+__device__ __forceinline__ Sum3 shfl_up3(const Sum3& a, int o) {
+  return {__shfl_up_sync(0xffffffffu, a.grow, o), __shfl_up_sync(0xffffffffu, a.drop, o),
+          __shfl_up_sync(0xffffffffu, a.add, o)};
+}
+
+// What a request asks for; a request whose lengths are impossible asks for nothing.
+struct Ask {
+  int have, want, add;
+  bool bad;
+};
+__device__ __forceinline__ Ask ask(const PageTablesParams& p, int len, int new_len) {
+  Ask a;
+  const int top = (1 << p.page_shift) - 1;
+  const long long cap = (long long)p.ld << p.page_shift;
+  a.bad = len < 0 || new_len < 0 || len > cap || new_len > cap;
+  a.have = a.bad ? 0 : (int)(((long long)len + top) >> p.page_shift);
+  a.want = a.bad ? 0 : (int)(((long long)new_len + top) >> p.page_shift);
+  a.add = a.bad ? 0 : max(0, new_len - len);
+  return a;
+}
+
+__global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTablesParams p) {
+  extern __shared__ int sm[];
+  int* s_cu = sm;                  // [B + 1] first new token of the request
+  int* s_len = s_cu + p.B + 1;     // [B] tokens before; -1: not served, its tokens get no slot
+  int* s_take = s_len + p.B;       // [B] ring entries taken by the requests before it
+  int* s_drop = s_take + p.B;      // [B] pages freed by the requests before it
+  __shared__ Sum3 s_warp[32];
+  __shared__ long long s_taken, s_freed;
+  __shared__ int s_bits;
+
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + kPtThreads - 1) / kPtThreads;  // consecutive requests of a thread
+  if (tid == 0) {
+    s_taken = 0;
+    s_bits = 0;
+  }
+  // the ring's state, made sane: head in [0, N), avail in [0, N]
+  const int head = (int)((((long long)p.free_in[0] % p.N) + p.N) % p.N);
+  const int avail = min(max(p.free_in[1], 0), p.N);
+
+  Sum3 mine = {0, 0, 0};
+  for (int k = 0; k < per; ++k) {
+    const int b = tid * per + k;
+    if (b >= p.B) break;
+    const int len = p.lens[b];
+    const Ask a = ask(p, len, p.new_lens[b]);
+    s_len[b] = len;
+    mine = mine + Sum3{max(0, a.want - a.have), max(0, a.have - a.want), a.add};
+  }
+  Sum3 upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sum3 t = shfl_up3(upto, o);
+    if (lane >= o) upto = upto + t;
+  }
+  if (lane == 31) s_warp[warp] = upto;
+  __syncthreads();
+  if (warp == 0) {
+    Sum3 w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const Sum3 t = shfl_up3(w, o);
+      if (lane >= o) w = w + t;
+    }
+    s_warp[lane] = w;
+    if (lane == 31) s_freed = w.drop;
+  }
+  __syncthreads();
+  Sum3 at = upto;  // exclusive sums of the thread's first request
+  if (warp > 0) at = at + s_warp[warp - 1];
+  at = {at.grow - mine.grow, at.drop - mine.drop, at.add - mine.add};
+
+  int bits = 0;
+  long long taken = 0;
+  for (int k = 0; k < per; ++k) {
+    const int b = tid * per + k;
+    if (b >= p.B) break;
+    const int len = s_len[b];
+    const Ask a = ask(p, len, p.new_lens[b]);
+    const int grow = max(0, a.want - a.have);
+    const bool served = !a.bad && (grow == 0 || at.grow + grow <= avail);
+    if (a.bad) bits |= BSA_PAGES_BAD_LENGTH;
+    else if (!served) bits |= BSA_PAGES_EXHAUSTED;
+    if (served && grow > 0) taken = at.grow + grow;
+    s_cu[b] = (int)min(at.add, (long long)INT_MAX);
+    s_take[b] = (int)min(at.grow, (long long)INT_MAX);
+    s_drop[b] = (int)min(at.drop, (long long)INT_MAX);
+    if (!served) s_len[b] = -1;
+    at = at + Sum3{grow, max(0, a.have - a.want), a.add};
+  }
+  if (tid == kPtThreads - 1) {  // its exclusive sum over all requests
+    s_cu[p.B] = (int)min(at.add, (long long)INT_MAX);
+    if (at.add > p.max_tokens) bits |= BSA_PAGES_TOKENS;
+  }
+  if (taken > 0) atomicMax((unsigned long long*)&s_taken, (unsigned long long)taken);
+  if (bits) atomicOr(&s_bits, bits);
+  __syncthreads();
+  const int freed = (int)min(s_freed, (long long)(p.N - avail));
+  if (tid == 0 && s_freed > freed) s_bits |= BSA_PAGES_RING;
+  cluster.sync();  // every CTA has read lens, new_lens and free
+
+  // pages that join and leave: a warp per request
+  for (int b = rank * 32 + warp; b < p.B; b += ranks * 32) {
+    const int new_len = p.new_lens[b];
+    const bool served = s_len[b] >= 0;
+    if (lane == 0) {
+      p.cu_new[b] = s_cu[b];
+      if (served) p.lens_out[b] = new_len;
+      else if (p.lens_out != p.lens) p.lens_out[b] = p.lens[b];
+    }
+    if (!served) continue;
+    const Ask a = ask(p, s_len[b], new_len);
+    int* row = p.table + (size_t)b * p.ld;
+    for (int i = lane; i < a.want - a.have; i += 32)
+      row[a.have + i] = p.ring[(int)(((long long)head + s_take[b] + i) % p.N)];
+    for (int i = lane; i < a.have - a.want; i += 32) {
+      const long long at_i = (long long)s_drop[b] + i;
+      if (at_i < freed) p.ring[(int)((head + avail + at_i) % p.N)] = row[a.want + i];
+    }
+  }
+
+  // slots and positions of the new tokens
+  const int total = s_cu[p.B];
+  for (int t0 = (rank * kPtThreads + tid) * 4; t0 < p.max_tokens; t0 += ranks * kPtThreads * 4) {
+    int lo = 0;  // the last request whose range starts at or before t0
+    if (t0 < total) {
+      int hi = p.B;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_cu[mid] <= t0) lo = mid; else hi = mid;
+      }
+    }
+    int slot[4], pos[4];
+    int page_at = -1, page_b = -1, id = -1;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int t = t0 + e;
+      slot[e] = pos[e] = -1;
+      if (t >= total) continue;
+      while (s_cu[lo + 1] <= t) ++lo;
+      const int len = s_len[lo];
+      if (len < 0) continue;
+      const int own = len + (t - s_cu[lo]);
+      const int c = own >> p.page_shift;
+      if (c != page_at || lo != page_b) {
+        const int have = (len + (1 << p.page_shift) - 1) >> p.page_shift;
+        id = c < have ? p.table[(size_t)lo * p.ld + c]
+                      : p.ring[(int)(((long long)head + s_take[lo] + (c - have)) % p.N)];
+        page_at = c;
+        page_b = lo;
+        if (id < 0 || id >= p.N) {
+          id = -1;
+          atomicOr(&s_bits, BSA_PAGES_BAD_ID);
+        }
+      }
+      if (id >= 0) slot[e] = (id << p.page_shift) + (own & ((1 << p.page_shift) - 1));
+      pos[e] = own + p.pos_offset;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (t0 + e >= p.max_tokens) break;
+      p.slots[t0 + e] = slot[e];
+      if (p.positions) p.positions[t0 + e] = pos[e];
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    if (rank == 0) {
+      p.cu_new[p.B] = total;
+      p.free_out[0] = (int)((head + s_taken) % p.N);
+      p.free_out[1] = (int)(avail - s_taken + freed);
+    }
+    if (s_bits && p.status) atomicOr(p.status, s_bits);
+  }
+}
+
+// K and V rows of new tokens to their slots; V is the chunk type (16 bytes, or one element when a
+// row does not start on a 16-byte boundary).
+template <typename V>
+__global__ void __launch_bounds__(256) paged_append_kernel(
+    const unsigned char* __restrict__ k, const unsigned char* __restrict__ v, long long k_stride,
+    long long v_stride, const int* __restrict__ slots, int T, int Hk, int row_shift,
+    int page_shift, int num_pages, V* __restrict__ kp, V* __restrict__ vp) {
+  // chunk c of head h of token t; a head's row has 1 << row_shift chunks
+  const int chunks = Hk << row_shift;
+  const long long n = (long long)T * chunks;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n;
+       i += (long long)gridDim.x * 256) {
+    const int t = (int)(i / chunks), hc = (int)(i - (long long)t * chunks);
+    const int slot = slots[t];
+    const V a = reinterpret_cast<const V*>(k + t * k_stride)[hc];
+    const V b = reinterpret_cast<const V*>(v + t * v_stride)[hc];
+    const int id = slot >> page_shift;
+    if (slot < 0 || id >= num_pages) continue;
+    const int h = hc >> row_shift, c = hc & ((1 << row_shift) - 1);
+    const long long row =
+        (((long long)id * Hk + h) << page_shift) + (slot & ((1 << page_shift) - 1));
+    kp[(row << row_shift) + c] = a;
+    vp[(row << row_shift) + c] = b;
+  }
+}
+
+template <typename V>
+void launch_append(const void* k, const void* v, long long ks, long long vs, const int* slots,
+                   int T, int Hk, int row_bytes, int page_shift, int num_pages, void* kp, void* vp,
+                   cudaStream_t st) {
+  int row_shift = 0;
+  while ((int)sizeof(V) << row_shift < row_bytes) ++row_shift;
+  const long long n = (long long)T * (Hk << row_shift);
+  const int grid = (int)std::min<long long>((n + 255) / 256, 8LL * kSMs * 4);
+  paged_append_kernel<V><<<grid, 256, 0, st>>>(
+      static_cast<const unsigned char*>(k), static_cast<const unsigned char*>(v), ks, vs, slots, T,
+      Hk, row_shift, page_shift, num_pages, static_cast<V*>(kp), static_cast<V*>(vp));
+}
+
+int page_shift_of(int page) {
+  for (int s = 4; s <= 7; ++s)
+    if (page == 1 << s) return s;
+  return -1;
+}
+
+}  // namespace
+}  // namespace bsa
+
+using namespace bsa;
+
+extern "C" bsa_status bsa_page_tables(int B, int page, const int* lens, const int* new_lens,
+                                      int* table, int table_ld, int* ring, int num_pages,
+                                      const int* free_in, int* lens_out, int* free_out,
+                                      int* cu_new, int* slots, int* positions, int max_tokens,
+                                      int pos_offset, int* status, void* stream) {
+  BSA_REQUIRE(B >= 0 && max_tokens >= 0 && table_ld >= 0 && page > 0 && num_pages >= 1,
+              BSA_ERR_ARG);
+  BSA_REQUIRE(free_in && free_out && cu_new && ring, BSA_ERR_ARG);
+  BSA_REQUIRE(B == 0 || (lens && new_lens && lens_out && (table || table_ld == 0)), BSA_ERR_ARG);
+  BSA_REQUIRE(slots || max_tokens == 0, BSA_ERR_ARG);
+  const int shift = page_shift_of(page);
+  BSA_REQUIRE(shift > 0 && B <= kPtMaxB, BSA_ERR_UNSUPPORTED);
+  // slots and a row's tokens are 32-bit
+  BSA_REQUIRE((long long)num_pages << shift <= INT_MAX && (long long)table_ld << shift <= INT_MAX,
+              BSA_ERR_UNSUPPORTED);
+  BSA_REQUIRE(pos_offset >= 0 && (long long)pos_offset + ((long long)table_ld << shift) <= INT_MAX,
+              BSA_ERR_ARG);
+  BSA_REQUIRE(max_tokens <= INT_MAX - kPtCluster * kPtThreads * 4, BSA_ERR_UNSUPPORTED);
+  PageTablesParams p = {B,    shift, table_ld, num_pages, max_tokens, pos_offset, lens, new_lens,
+                        table, ring, free_in,  lens_out,  free_out,   cu_new,     slots, positions,
+                        status};
+  const int smem = (4 * B + 1) * (int)sizeof(int);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+          cudaSuccess) {
+    (void)cudaGetLastError();
+    return BSA_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  const unsigned ctas = (long long)B + max_tokens <= kPtOneCta ? 1u : (unsigned)kPtCluster;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kPtThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, page_tables_kernel, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return BSA_ERR_CUDA;
+  }
+  return BSA_OK;
+}
+
+extern "C" bsa_status bsa_paged_append(const void* k, const void* v, bsa_dtype dt, int T, int Hk,
+                                       int d, long long k_stride, long long v_stride,
+                                       const int* slots, int page, int num_pages, void* k_pages,
+                                       void* v_pages, void* stream) {
+  BSA_REQUIRE(T >= 0 && Hk > 0 && d > 0 && page > 0 && num_pages >= 1, BSA_ERR_ARG);
+  BSA_REQUIRE(dtype_ok(dt), BSA_ERR_DTYPE);
+  BSA_REQUIRE(T == 0 || (k && v && slots && k_pages && v_pages), BSA_ERR_ARG);
+  const int shift = page_shift_of(page);
+  BSA_REQUIRE(head_dim_ok(d) && shift > 0, BSA_ERR_UNSUPPORTED);
+  BSA_REQUIRE((long long)num_pages << shift <= INT_MAX && Hk <= 4096, BSA_ERR_UNSUPPORTED);
+  BSA_REQUIRE(T <= 1 || (k_stride >= (long long)Hk * d && v_stride >= (long long)Hk * d),
+              BSA_ERR_SHAPE);
+  BSA_REQUIRE(all_aligned16(k_pages, v_pages), BSA_ERR_ARG);
+  if (T == 0) return BSA_OK;
+  const int es = dt == BSA_BF16 ? 2 : 4;
+  BSA_REQUIRE(((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & (es - 1)) == 0,
+              BSA_ERR_ARG);
+  const long long ks = k_stride * es, vs = v_stride * es;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (all_aligned16(k, v) && (T == 1 || (ks % 16 == 0 && vs % 16 == 0)))
+    launch_append<uint4>(k, v, ks, vs, slots, T, Hk, d * es, shift, num_pages, k_pages, v_pages,
+                         st);
+  else if (es == 2)
+    launch_append<uint16_t>(k, v, ks, vs, slots, T, Hk, d * es, shift, num_pages, k_pages, v_pages,
+                            st);
+  else
+    launch_append<uint32_t>(k, v, ks, vs, slots, T, Hk, d * es, shift, num_pages, k_pages, v_pages,
+                            st);
+  BSA_LAUNCH_CHECK();
+  return BSA_OK;
+}

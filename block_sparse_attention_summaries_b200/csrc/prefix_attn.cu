@@ -1,0 +1,412 @@
+// Attention of a batch that shares a long prefix, over a paged K/V cache (bsa_prefix_attn).
+//
+// Token t, the i-th of nq new tokens of request b, sits at own position p = lens[b] - nq + i and
+// sees every key of the prefix and its request's own keys j <= p:
+//     o = sum_j softmax_j(q . k_j / sqrt(d)) v_j,   lse = log sum_j exp(q . k_j / sqrt(d)).
+// A softmax over two sets of keys joins from each set's maximum m, sum l and weighted values a:
+//     M = max(m1, m2),  l = l1 2^(m1 - M) + l2 2^(m2 - M),  o = (a1 2^(m1 - M) + a2 2^(m2 - M)) / l
+// (log2 units), so the prefix is attended once for the rows of ALL requests -- packed, token after
+// token, into full query tiles, whose keys are then read once per tile and not once per request --
+// and each request's own keys only for its own rows.  Both parts may be cut into pieces along the
+// keys when there are too few tiles to fill the GPU; prefix_merge_kernel joins a row's pieces.
+//
+// prefix_simt_kernel: any type, CUDA cores.  A CTA of 256 threads takes RG rows (of one kv head,
+// row = token * G + head of the group) and a piece of the keys in tiles of 64: S = Q K^T in
+// registers from shared memory, online softmax with the running maximum and sum of each row in
+// registers of the 16 threads that share it, P through shared memory, O += P V in registers.
+#include "prefix_attn.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kPsThreads = 256;
+constexpr int kPsKeys = 64;  // keys of a tile
+
+template <int D, int RG>
+struct SimtSmem {
+  static constexpr int kLd = D + 4;  // floats; rows 4 banks apart
+  static constexpr int kLdP = kPsKeys + 4;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + RG * kLd;
+  static constexpr int kV = kK + kPsKeys * kLd;
+  static constexpr int kP = kV + kPsKeys * kLd;
+  static constexpr int kTotal = (kP + RG * kLdP) * (int)sizeof(float);
+};
+
+struct SimtGrid {
+  int units1;  // CTAs of the prefix: tiles of packed rows x kv heads x pieces
+  int tiles2;  // row tiles of a request
+};
+
+template <typename T, int D, int RG>
+__global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixParams p,
+                                                                 const SimtGrid g) {
+  using L = SimtSmem<D, RG>;
+  constexpr int TM = RG / 16;  // rows of a thread
+  constexpr int DC = D / 64;   // float4 columns of a thread
+  extern __shared__ __align__(16) float smf[];
+  float *sq = smf + L::kQ, *sk = smf + L::kK, *sv = smf + L::kV, *sp = smf + L::kP;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+
+  // the unit: rows r0 .. r0 + nrows of kv head h (row = token * G + head of the group), keys
+  // [0, n) on `pages`; row r sees keys j <= first_pos + r / G
+  int u = blockIdx.x, h, nrows, r0, n, slot, piece, pieces;
+  long long first_pos;
+  const int* pages;
+  if (u < g.units1) {
+    piece = u % p.ns1;
+    u /= p.ns1;
+    h = u % p.Hk;
+    r0 = u / p.Hk * RG;
+    nrows = min(RG, pa_tokens(p) * p.G - r0);
+    pages = p.ptable;
+    n = p.prefix_len;
+    first_pos = n;
+    slot = piece;
+    pieces = p.ns1;
+  } else {
+    u -= g.units1;
+    piece = u % p.ns2;
+    u /= p.ns2;
+    h = u % p.Hk;
+    u /= p.Hk;
+    const int tile = u % g.tiles2, b = u / g.tiles2;
+    const PaRequest r = pa_request(p, b);
+    r0 = r.t0 * p.G + tile * RG;
+    nrows = min(RG, min(r.nq, p.max_q) * p.G - tile * RG);
+    pages = p.table + (size_t)b * p.table_ld;
+    // tiles start at whole tokens: G divides RG
+    first_pos = (long long)r.len - r.nq + tile * (RG / p.G);
+    n = (int)max(0ll, min((long long)r.len, first_pos + (nrows - 1) / p.G + 1));
+    slot = p.ns1 + piece;
+    pieces = p.ns2;
+  }
+  if (nrows <= 0) return;
+  const int tiles = (n + kPsKeys - 1) / kPsKeys, per = (tiles + pieces - 1) / pieces;
+  const int tile0 = min(piece * per, tiles), tile1 = min(tile0 + per, tiles);
+
+  const long long rows = (long long)p.T * p.Hq;
+  auto row_id = [&](int r) {  // of the partial results: token * Hq + query head
+    const int rr = r0 + r;
+    return (long long)(rr / p.G) * p.Hq + h * p.G + rr % p.G;
+  };
+  float m[TM], l[TM], acc[TM][DC * 4];
+#pragma unroll
+  for (int a = 0; a < TM; ++a) {
+    m[a] = -INFINITY;
+    l[a] = 0.f;
+#pragma unroll
+    for (int c = 0; c < DC * 4; ++c) acc[a][c] = 0.f;
+  }
+  if (tile0 < tile1) {
+    // queries, scaled to log2 units
+    const float scale = rsqrtf((float)D) * kPaLog2e;
+    for (int i = tid; i < RG * (D / 4); i += kPsThreads) {
+      const int r = i / (D / 4), c = i % (D / 4) * 4;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      if (r < nrows) {
+        const int rr = r0 + r;
+        load_vec<T, 4>(static_cast<const T*>(p.q) + (rr / p.G) * p.q_stride +
+                           (long long)(h * p.G + rr % p.G) * D + c, x);
+      }
+      *reinterpret_cast<float4*>(sq + r * L::kLd + c) =
+          make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale);
+    }
+  }
+  for (int tile = tile0; tile < tile1; ++tile) {
+    const int j0 = tile * kPsKeys;
+    __syncthreads();  // the previous tile is read
+    for (int i = tid; i < kPsKeys * (D / 4); i += kPsThreads) {
+      const int j = i / (D / 4), c = i % (D / 4) * 4;
+      float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+      if (j0 + j < n) {
+        const int id = pages[(j0 + j) >> p.page_shift];
+        if (id >= 0 && id < p.num_pages) {
+          const long long at = (((((long long)id * p.Hk + h) << p.page_shift) +
+                                 ((j0 + j) & ((1 << p.page_shift) - 1))) * D) + c;
+          load_vec<T, 4>(static_cast<const T*>(p.k) + at, x);
+          load_vec<T, 4>(static_cast<const T*>(p.v) + at, y);
+        }
+      }
+      *reinterpret_cast<float4*>(sk + j * L::kLd + c) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4*>(sv + j * L::kLd + c) = make_float4(y[0], y[1], y[2], y[3]);
+    }
+    __syncthreads();
+    // scores of keys tx + 16 e
+    float s[TM][4];
+#pragma unroll
+    for (int a = 0; a < TM; ++a)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[a][e] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+      float4 kk[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        kk[e] = *reinterpret_cast<const float4*>(sk + (tx + 16 * e) * L::kLd + c);
+#pragma unroll
+      for (int a = 0; a < TM; ++a) {
+        const float4 qq = *reinterpret_cast<const float4*>(sq + (ty * TM + a) * L::kLd + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[a][e] += qq.x * kk[e].x + qq.y * kk[e].y + qq.z * kk[e].z + qq.w * kk[e].w;
+      }
+    }
+    uint32_t live = 0;  // keys tx + 16 e of the tile that exist: in range, on a page of the pool
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + tx + 16 * e;
+      if (j < n) {
+        const int id = pages[j >> p.page_shift];
+        if (id >= 0 && id < p.num_pages) live |= 1u << e;
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < TM; ++a) {
+      const long long last = first_pos + (ty * TM + a) / p.G;
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!((live >> e) & 1) || j0 + tx + 16 * e > last) s[a][e] = -INFINITY;
+        top = fmaxf(top, s[a][e]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float m_new = fmaxf(m[a], top);
+      const float base = m_new == -INFINITY ? 0.f : m_new;
+      const float corr = exp2f(m[a] - base);
+      m[a] = m_new;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float pe = exp2f(s[a][e] - base);
+        sp[(ty * TM + a) * L::kLdP + tx + 16 * e] = pe;
+        sum += pe;
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l[a] = l[a] * corr + sum;
+#pragma unroll
+      for (int c = 0; c < DC * 4; ++c) acc[a][c] *= corr;
+    }
+    __syncwarp();  // a row's P is written and read by the 16 threads of its half warp
+#pragma unroll 2
+    for (int j = 0; j < kPsKeys; j += 4) {
+      float pj[TM][4];
+#pragma unroll
+      for (int a = 0; a < TM; ++a) {
+        const float4 t = *reinterpret_cast<const float4*>(sp + (ty * TM + a) * L::kLdP + j);
+        pj[a][0] = t.x; pj[a][1] = t.y; pj[a][2] = t.z; pj[a][3] = t.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int c = 0; c < DC; ++c) {
+          const float4 vv =
+              *reinterpret_cast<const float4*>(sv + (j + e) * L::kLd + tx * 4 + 64 * c);
+#pragma unroll
+          for (int a = 0; a < TM; ++a) {
+            // a key that the row does not see adds nothing, whatever its value holds
+            const float w = pj[a][e];
+            acc[a][4 * c] = w == 0.f ? acc[a][4 * c] : fmaf(w, vv.x, acc[a][4 * c]);
+            acc[a][4 * c + 1] = w == 0.f ? acc[a][4 * c + 1] : fmaf(w, vv.y, acc[a][4 * c + 1]);
+            acc[a][4 * c + 2] = w == 0.f ? acc[a][4 * c + 2] : fmaf(w, vv.z, acc[a][4 * c + 2]);
+            acc[a][4 * c + 3] = w == 0.f ? acc[a][4 * c + 3] : fmaf(w, vv.w, acc[a][4 * c + 3]);
+          }
+        }
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < TM; ++a) {
+    const int r = ty * TM + a;
+    if (r >= nrows) continue;
+    const long long at = (long long)slot * rows + row_id(r);
+    if (tx == 0) p.part_ml[at] = make_float2(m[a], l[a]);
+    if (l[a] == 0.f) continue;  // no key (scores of NaN leave the maximum at -inf and l at NaN)
+#pragma unroll
+    for (int c = 0; c < DC; ++c)
+      *reinterpret_cast<float4*>(p.part_o + at * D + tx * 4 + 64 * c) =
+          make_float4(acc[a][4 * c], acc[a][4 * c + 1], acc[a][4 * c + 2], acc[a][4 * c + 3]);
+  }
+}
+
+// Joins the pieces of a row: a warp per row, d / 32 columns per lane.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p) {
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long rows = (long long)p.T * p.Hq;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int t = (int)(row / p.Hq);
+  if (t >= pa_tokens(p)) return;
+  if (p.cu_q) {
+    // the request of the token: how many requests end at or before it
+    int b = 0;
+    for (int i = 0; i < p.B; i += 32) {
+      const bool before = i + lane < p.B && p.cu_q[i + lane + 1] <= t;
+      b += __popc(__ballot_sync(0xffffffffu, before));
+    }
+    // tokens beyond max_q of their request were not attended
+    if (b >= p.B || t - p.cu_q[b] >= p.max_q) return;
+  }
+  const int ns = p.ns1 + p.ns2;
+  float top = -INFINITY;
+  for (int s = lane; s < ns; s += 32) top = fmaxf(top, p.part_ml[s * rows + row].x);
+  top = warp_max(top);
+  float acc[C], l = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  for (int s = 0; s < ns; ++s) {
+    const float2 ml = p.part_ml[s * rows + row];
+    if (ml.y == 0.f) continue;
+    const float w = exp2f(ml.x - top);
+    float x[C];
+    load_vec<float, C>(p.part_o + (s * rows + row) * D + lane * C, x);
+    l += ml.y * w;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] += x[c] * w;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // no key at all: o = 0
+  T* op = static_cast<T*>(p.o) + row * D + lane * C;
+  if constexpr (sizeof(T) == 2) {
+    __nv_bfloat162 w[C / 2];
+#pragma unroll
+    for (int c = 0; c < C; c += 2) w[c / 2] = __floats2bfloat162_rn(acc[c] * inv, acc[c + 1] * inv);
+    if constexpr (C == 4) *reinterpret_cast<uint2*>(op) = *reinterpret_cast<uint2*>(w);
+    else *reinterpret_cast<uint32_t*>(op) = *reinterpret_cast<uint32_t*>(w);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; c += 2)
+      *reinterpret_cast<float2*>(op + c) = make_float2(acc[c] * inv, acc[c + 1] * inv);
+  }
+  if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kPaLn2;
+}
+
+// How the keys are cut: enough pieces that the CTAs fill the GPU twice, none under 4 tiles.
+int pieces_for(long long units, long long tiles) {
+  const long long want = (2LL * kSMs + units - 1) / std::max(1LL, units);
+  return (int)std::max(1LL, std::min(std::min(want, tiles / 4), 64LL));
+}
+
+struct PrefixPlan {
+  int rg, tiles1, tiles2, ns1, ns2;
+  size_t ml_bytes, o_bytes;
+};
+
+PrefixPlan plan_of(int T, int B, int Hq, int Hk, int d, int page, int table_ld, int prefix_len,
+                   int max_q) {
+  PrefixPlan w;
+  const int G = Hq / Hk;
+  w.rg = (long long)max_q * G <= 16 ? 16 : 64;
+  const long long rows = (long long)T * G;
+  w.tiles1 = (int)((rows + w.rg - 1) / w.rg);
+  w.tiles2 = (int)(((long long)max_q * G + w.rg - 1) / w.rg);
+  const long long keys2 = (long long)table_ld * page;
+  w.ns1 = prefix_len ? pieces_for((long long)w.tiles1 * Hk, (prefix_len + 63) / 64) : 0;
+  w.ns2 = keys2 ? pieces_for((long long)w.tiles2 * B * Hk, (keys2 + 63) / 64) : 0;
+  const long long all = (long long)T * Hq * (w.ns1 + w.ns2);
+  w.ml_bytes = align_up((size_t)all * sizeof(float2), 256);
+  w.o_bytes = (size_t)all * d * sizeof(float);
+  return w;
+}
+
+template <typename T, int D, int RG>
+bsa_status launch_simt(const PrefixParams& p, const PrefixPlan& w, cudaStream_t st) {
+  const long long units1 = p.ns1 ? (long long)w.tiles1 * p.Hk * p.ns1 : 0;
+  const long long units2 = (long long)p.B * w.tiles2 * p.Hk * p.ns2;
+  if (units1 + units2 > INT_MAX) return BSA_ERR_UNSUPPORTED;
+  if (units1 + units2 > 0) {
+    auto kern = prefix_simt_kernel<T, D, RG>;
+    const int smem = SimtSmem<D, RG>::kTotal;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        cudaSuccess) {
+      (void)cudaGetLastError();
+      return BSA_ERR_CUDA;
+    }
+    kern<<<(int)(units1 + units2), kPsThreads, smem, st>>>(p, SimtGrid{(int)units1, w.tiles2});
+    BSA_LAUNCH_CHECK();
+  }
+  const long long rows = (long long)p.T * p.Hq;
+  prefix_merge_kernel<T, D><<<(int)((rows + 7) / 8), 256, 0, st>>>(p);
+  BSA_LAUNCH_CHECK();
+  return BSA_OK;
+}
+
+bool sizes_ok(int T, int B, int Hq, int Hk, int d, int page, int table_ld, int prefix_len,
+              int max_q) {
+  return T >= 0 && B >= 0 && Hq > 0 && Hk > 0 && d > 0 && page > 0 && table_ld >= 0 &&
+         prefix_len >= 0 && max_q > 0;
+}
+bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+int page_shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+}  // namespace
+}  // namespace bsa
+
+using namespace bsa;
+
+extern "C" size_t bsa_prefix_attn_workspace_bytes(bsa_dtype dt, int T, int B, int Hq, int Hk,
+                                                  int d, int page, int table_ld, int prefix_len,
+                                                  int max_q) {
+  if (!dtype_ok(dt) || !sizes_ok(T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q) ||
+      !head_dim_ok(d) || !group_ok(Hq, Hk) || !page_ok(page))
+    return 0;
+  const PrefixPlan w = plan_of(T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q);
+  return w.ml_bytes + w.o_bytes;
+}
+
+extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const void* k_pages,
+                                      const void* v_pages, bsa_dtype dt, int T, int B, int Hq,
+                                      int Hk, int d, int page, int num_pages, const int* table,
+                                      int table_ld, const int* lens, const int* prefix_table,
+                                      int prefix_len, const int* cu_q, int max_q, void* o,
+                                      float* lse, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  BSA_REQUIRE(sizes_ok(T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q) && num_pages >= 1,
+              BSA_ERR_ARG);
+  BSA_REQUIRE(dtype_ok(dt), BSA_ERR_DTYPE);
+  BSA_REQUIRE(T == 0 || B == 0 || (q && k_pages && v_pages && lens && o), BSA_ERR_ARG);
+  BSA_REQUIRE(prefix_len == 0 || prefix_table, BSA_ERR_ARG);
+  BSA_REQUIRE(table_ld == 0 || B == 0 || table, BSA_ERR_ARG);
+  BSA_REQUIRE(Hq % Hk == 0, BSA_ERR_SHAPE);
+  BSA_REQUIRE(cu_q || (T == B && max_q == 1), BSA_ERR_SHAPE);
+  BSA_REQUIRE(max_q <= std::max(T, 1), BSA_ERR_SHAPE);
+  BSA_REQUIRE(group_ok(Hq, Hk) && head_dim_ok(d) && page_ok(page), BSA_ERR_UNSUPPORTED);
+  // rows of the pool and of the packed queries, and a request's tokens, are 32-bit
+  BSA_REQUIRE((long long)num_pages * Hk * page <= INT_MAX && (long long)T * Hq <= INT_MAX &&
+                  (long long)table_ld * page <= INT_MAX, BSA_ERR_UNSUPPORTED);
+  BSA_REQUIRE(T <= 1 || q_stride >= (long long)Hq * d, BSA_ERR_SHAPE);
+  const int es = dt == BSA_BF16 ? 2 : 4;
+  BSA_REQUIRE(all_aligned16(q, k_pages, v_pages, o) && (T <= 1 || q_stride * es % 16 == 0),
+              BSA_ERR_ARG);
+  if (T == 0 || B == 0) return BSA_OK;
+  const PrefixPlan w = plan_of(T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q);
+  const size_t need = w.ml_bytes + w.o_bytes;
+  BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), BSA_ERR_WORKSPACE);
+  BSA_REQUIRE(aligned16(workspace), BSA_ERR_ARG);
+  PrefixParams p;
+  p.q = q; p.k = k_pages; p.v = v_pages;
+  p.q_stride = T <= 1 ? (long long)Hq * d : q_stride;
+  p.T = T; p.B = B; p.Hq = Hq; p.Hk = Hk; p.G = Hq / Hk;
+  p.page_shift = page_shift_of(page);
+  p.num_pages = num_pages;
+  p.table = table; p.table_ld = table_ld; p.lens = lens;
+  p.ptable = prefix_table; p.prefix_len = prefix_len;
+  p.cu_q = cu_q; p.max_q = max_q;
+  p.o = o; p.lse = lse;
+  p.part_ml = static_cast<float2*>(workspace);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.ml_bytes);
+  p.ns1 = w.ns1; p.ns2 = w.ns2;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto go = [&](auto type, auto dim) {
+    using E = decltype(type);
+    constexpr int D = decltype(dim)::value;
+    return w.rg == 16 ? launch_simt<E, D, 16>(p, w, st) : launch_simt<E, D, 64>(p, w, st);
+  };
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  if (dt == BSA_BF16)
+    return d == 64 ? go(__nv_bfloat16(), D64()) : go(__nv_bfloat16(), D128());
+  return d == 64 ? go(float(), D64()) : go(float(), D128());
+}

@@ -1,0 +1,55 @@
+// Shared by the kernels of bsa_prefix_attn: the call's parameters, the requests' ranges, and the
+// partial results that the merge kernel joins.
+#pragma once
+
+#include "bsa_common.cuh"
+
+namespace bsa {
+
+constexpr float kPaLog2e = 1.4426950408889634f;
+constexpr float kPaLn2 = 0.6931471805599453f;
+
+struct PrefixParams {
+  const void *q, *k, *v;  // q [T, Hq, d] with token stride q_stride; pools [P, Hk, page, d]
+  long long q_stride;     // elements
+  int T, B, Hq, Hk, G, page_shift, num_pages;
+  const int* table;  // [B, table_ld] pages of each request's own tokens
+  int table_ld;
+  const int* lens;    // [B] own tokens, the new ones included
+  const int* ptable;  // pages of the prefix
+  int prefix_len;
+  const int* cu_q;  // [B + 1] or null: one new token per request
+  int max_q;
+  void* o;
+  float* lse;
+  // Partial results: slots [0, ns1) hold the pieces of the prefix, [ns1, ns1 + ns2) those of the
+  // own tokens; part_o [slot][T * Hq][d] unnormalised, part_ml [slot][T * Hq] = (row maximum in
+  // log2 units, row sum).  A row without keys in a piece has sum 0 and no part_o.
+  float* part_o;
+  float2* part_ml;
+  int ns1, ns2;
+};
+
+// Request b: its first new token, how many it has, its own tokens.  Values that would reach
+// outside the call's arrays are cut.
+struct PaRequest {
+  int t0, nq, len;
+};
+__device__ __forceinline__ PaRequest pa_request(const PrefixParams& p, int b) {
+  PaRequest r;
+  if (p.cu_q) {
+    r.t0 = min(max(p.cu_q[b], 0), p.T);
+    r.nq = min(max(p.cu_q[b + 1], r.t0), p.T) - r.t0;
+  } else {
+    r.t0 = b;
+    r.nq = 1;
+  }
+  r.len = min(max(p.lens[b], 0), p.table_ld << p.page_shift);
+  return r;
+}
+// New tokens in all: rows at or after this are left as they were.
+__device__ __forceinline__ int pa_tokens(const PrefixParams& p) {
+  return p.cu_q ? min(max(p.cu_q[p.B], 0), p.T) : p.B;
+}
+
+}  // namespace bsa

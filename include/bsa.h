@@ -498,6 +498,102 @@ bsa_status bsa_freesolo_attn(const void* q, const void* k, const void* v, bsa_dt
 size_t bsa_freesolo_workspace_bytes(bsa_dtype dt, int B, int H, int n, int d, int cell, int K);
 
 /*
+ * Paged serving: requests that share a prefix
+ * -------------------------------------------
+ * The calls below keep K and V in a pool of pages, [num_pages, Hk, page, d] each (page = 16, 32, 64
+ * or 128 tokens), instead of one dense [B, Hk, n, d] cache: a request owns the pages its table row
+ * lists, in order, and all requests of a batch read the pages of a common prefix (a system prompt,
+ * a document), which are stored once.  They serve the layers that keep full attention beside the
+ * block-sparse ones.  The pages cited above have no counterpart to them.  A serving step is
+ *     bsa_page_tables -> bsa_paged_append -> bsa_prefix_attn
+ * on one stream; nothing in it reads device memory on the host, so it can be captured into a graph.
+ */
+
+/* What bsa_page_tables reports in *status (bits). */
+typedef enum {
+  BSA_PAGES_EXHAUSTED = 1,  /* too few free pages: the requests that did not fit are unchanged */
+  BSA_PAGES_BAD_LENGTH = 2, /* a length below 0 or above table_ld * page: the request is unchanged */
+  BSA_PAGES_RING = 4,       /* more pages were freed than the ring has room for: they are dropped */
+  BSA_PAGES_TOKENS = 8,     /* more new tokens than max_tokens: the further ones get no slot */
+  BSA_PAGES_BAD_ID = 16     /* a page id outside the pool: its tokens get slot -1 */
+} bsa_pages_status;
+
+/*
+ * bsa_page_tables -- one step of the page tables and slot maps from the requests' lengths.
+ *   lens, new_lens [B] int32: tokens each request has and is to have.  A growing request takes
+ *             pages from the ring, a shrinking one returns them (new length 0: the request is done).
+ *   table     [B, table_ld] int32, in/out: new entries are written, all others kept (entries at or
+ *             past ceil(length / page) mean nothing).
+ *   ring      [num_pages] int32, in/out, and free_in [2] = {head, avail}: the free pages are
+ *             ring[(head + i) % num_pages], i < avail.  Pages are taken from the front, request after
+ *             request, and returned to the end; returned ones can be taken from the next call on.
+ *   With have = ceil(lens / page) and grow = max(0, ceil(new_lens / page) - have), request b is
+ *   served iff grow = 0 or the sum of grow over requests 0..b is at most avail; one that is not
+ *   keeps its length and pages, and its tokens get no slots.
+ *   lens_out  [B] out: the lengths after the step.  free_out [2] out: {head, avail} after it.
+ *   cu_new    [B + 1] out: exclusive sum of max(0, new_lens - lens): where each request's new
+ *             tokens start in the step's packed token arrays.
+ *   slots     [max_tokens] out: page * (page id) + offset of every new token, -1 where there is none.
+ *   positions [max_tokens] optional out: pos_offset + the token's own position (pos_offset: the
+ *             length of the shared prefix), -1 where there is none.
+ *   status    optional device int: bsa_pages_status bits are or-ed into it.
+ * lens_out may be lens or new_lens, and free_out may be free_in (a state advanced in place).
+ * Limits: B <= 8192, num_pages * page < 2^31.  Deterministic; one launch.
+ */
+bsa_status bsa_page_tables(int B, int page, const int* lens, const int* new_lens, int* table,
+                           int table_ld, int* ring, int num_pages, const int* free_in,
+                           int* lens_out, int* free_out, int* cu_new, int* slots, int* positions,
+                           int max_tokens, int pos_offset, int* status, void* stream);
+
+/*
+ * bsa_paged_append -- write the keys and values of T new tokens to their slots.
+ *   k, v      [T, Hk, d] (dtype dt): the heads of a token are contiguous, tokens are k_stride /
+ *             v_stride elements apart (slices of a fused projection); any element alignment.
+ *   slots     [T] int32 as written by bsa_page_tables; a slot outside [0, num_pages * page) is
+ *             skipped.  No two tokens may have the same slot.
+ *   k_pages, v_pages [num_pages, Hk, page, d], 16-byte aligned; rows of other slots are kept.
+ */
+bsa_status bsa_paged_append(const void* k, const void* v, bsa_dtype dt, int T, int Hk, int d,
+                            long long k_stride, long long v_stride, const int* slots, int page,
+                            int num_pages, void* k_pages, void* v_pages, void* stream);
+
+/*
+ * bsa_prefix_attn -- exact attention of a batch that shares a prefix, the prefix computed once for
+ * all requests.  The i-th of request b's nq new tokens sits at own position p = lens[b] - nq + i
+ * and sees all prefix_len keys of the prefix and its request's own keys j <= p:
+ *     o = sum_j softmax_j(q . k_j / sqrt(d)) v_j,   lse = log sum_j exp(q . k_j / sqrt(d)).
+ *   q         [T, Hq, d]: the new tokens, packed request after request; the heads of a token are
+ *             contiguous, tokens are q_stride elements apart (a multiple of 16 bytes).
+ *   k_pages, v_pages [num_pages, Hk, page, d] (the new tokens' keys and values already in them).
+ *   table [B, table_ld], lens [B]: the requests' own pages and tokens, the new ones included.
+ *   prefix_table [ceil(prefix_len / page)], prefix_len: the prefix, of any length (a request's own
+ *             tokens start on a page of their own); 0 = none.
+ *   cu_q      [B + 1] int32: first new token of each request (bsa_page_tables writes it), or NULL:
+ *             one token per request (T = B, max_q = 1).
+ *   max_q     the most new tokens any request has, <= T.
+ *   o [T, Hq, d] out; lse [T, Hq] optional out.  A token that sees no key gets o = 0, lse = -inf.
+ *             Rows at or after cu_q[B], and tokens beyond the max_q-th of a request, are left as
+ *             they were.
+ *   workspace device scratch of bsa_prefix_attn_workspace_bytes() bytes, 16-byte aligned; needs no
+ *             initialisation and may be reused once the stream has passed the call.  Calls that
+ *             share one must not run at the same time.
+ * Keys and values that no position reaches (the rest of a last page, other pages of the pool) are
+ * not used, whatever they hold.  A page id outside the pool is not read: its tokens take no part.
+ * Sums, softmax statistics and partial results are float32; with bf16 inputs the softmax weights
+ * are rounded to bf16 for the product with V.  Limits: num_pages * Hk * page and T * Hq < 2^31.
+ */
+bsa_status bsa_prefix_attn(const void* q, long long q_stride, const void* k_pages,
+                           const void* v_pages, bsa_dtype dt, int T, int B, int Hq, int Hk, int d,
+                           int page, int num_pages, const int* table, int table_ld,
+                           const int* lens, const int* prefix_table, int prefix_len,
+                           const int* cu_q, int max_q, void* o, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Workspace bytes bsa_prefix_attn needs for these sizes (0 for unsupported ones). */
+size_t bsa_prefix_attn_workspace_bytes(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page,
+                                       int table_ld, int prefix_len, int max_q);
+
+/*
  * bsa_sparse_attn_decode_noalloc -- the decode form of bsa_sparse_attn_fwd (nq == 1) for callers
  * that cannot provide device memory: an engine that plans all device memory ahead and forbids
  * any other allocation, or a plugin whose host framework owns the allocator and gives it none.

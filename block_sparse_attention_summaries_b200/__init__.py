@@ -72,7 +72,7 @@ SIGNATURES = [
     ("bsa_paged_append", _I, [_P, _P, _I, _I, _I, _I, ctypes.c_longlong, ctypes.c_longlong, _P, _I,
                               _I, _P, _P, _P]),
     ("bsa_prefix_attn", _I, [_P, ctypes.c_longlong, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I,
-                             _P, _P, _I, _P, _I, _P, _P, _P, _Z, _P]),
+                             _P, _P, _I, _P, _I, _P, _P, _P, _P, _Z, _P]),
     ("bsa_prefix_attn_workspace_bytes", _Z, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I]),
     ("bsa_workspace_status", _I, [_P, _P]),
     ("bsa_selftest_bounded_wait", _I, [_P, _I, _P]),
@@ -807,7 +807,7 @@ def prefix_attn_workspace_bytes(dtype, T, B, Hq, Hk, d, page, table_ld, prefix_l
 
 
 def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q=None, max_q=1,
-                o=None, lse=None, ws=None):
+                o=None, lse=None, ws=None, status=None):
     """Attention of a batch behind a shared prefix, over pages (bsa_prefix_attn).
 
     q [T, Hq, d]: the new tokens, packed (tokens may be strided); k_pages, v_pages
@@ -815,7 +815,8 @@ def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q
     ones included; prefix_table, prefix_len: the shared prefix (prefix_table may be None when
     prefix_len is 0).  cu_q [B + 1]: first new token of each request, with max_q the most any
     request has; None: one token per request.  ``ws``: a uint8 device tensor of at least
-    prefix_attn_workspace_bytes bytes (allocated here when None).  Returns (o, lse)."""
+    prefix_attn_workspace_bytes bytes (allocated here when None).  ``status`` (int32 [1], optional):
+    set nonzero if a bounded device wait ran out.  Returns (o, lse)."""
     dev = q.device
     q_stride = _heads(q, "q")
     T, Hq, d = q.shape
@@ -845,11 +846,11 @@ def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q
         ws = torch.empty(h.bsa_prefix_attn_workspace_bytes(dt, T, B, Hq, Hk, d, page, table_ld,
                                                            prefix_len, max_q),
                          device=dev, dtype=torch.uint8)
-    _on_device(dev, k_pages, v_pages, table, lens, prefix_table, cu_q, o, lse, ws)
-    _ints(table, lens, prefix_table, cu_q)
+    _on_device(dev, k_pages, v_pages, table, lens, prefix_table, cu_q, o, lse, ws, status)
+    _ints(table, lens, prefix_table, cu_q, status)
     _call(h.bsa_prefix_attn, dev, "bsa_prefix_attn", q.data_ptr(), q_stride, k_pages.data_ptr(),
           v_pages.data_ptr(), dt, T, B, Hq, Hk, d, page, P, table.data_ptr(), table_ld,
           lens.data_ptr(), None if prefix_table is None else prefix_table.data_ptr(), prefix_len,
           None if cu_q is None else cu_q.data_ptr(), max_q, o.data_ptr(), lse.data_ptr(),
-          ws.data_ptr(), ws.numel())
+          None if status is None else status.data_ptr(), ws.data_ptr(), ws.numel())
     return o, lse

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
   // the unit: rows r0 .. r0 + nrows of kv head h (row = token * G + head of the group), keys
   // [0, n) on `pages`; row r sees keys j <= first_pos + r / G
   int u = blockIdx.x, h, nrows, r0, n, slot, piece, pieces;
-  long long first_pos;
+  int first_pos;
   const int* pages;
   if (u < g.units1) {
     piece = u % p.ns1;
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
     nrows = min(RG, min(r.nq, p.max_q) * p.G - tile * RG);
     pages = p.table + (size_t)b * p.table_ld;
     // tiles start at whole tokens: G divides RG
-    first_pos = (long long)r.len - r.nq + tile * (RG / p.G);
-    n = (int)max(0ll, min((long long)r.len, first_pos + (nrows - 1) / p.G + 1));
+    first_pos = r.len - r.nq + tile * (RG / p.G);
+    n = max(0, min(r.len, first_pos + (nrows - 1) / p.G + 1));
     slot = p.ns1 + piece;
     pieces = p.ns2;
   }
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
     }
 #pragma unroll
     for (int a = 0; a < TM; ++a) {
-      const long long last = first_pos + (ty * TM + a) / p.G;
+      const int last = first_pos + (ty * TM + a) / p.G;
       float top = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -283,29 +283,51 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p)
   if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kPaLn2;
 }
 
-// How the keys are cut: enough pieces that the CTAs fill the GPU twice, none under 4 tiles.
-int pieces_for(long long units, long long tiles) {
-  const long long want = (2LL * kSMs + units - 1) / std::max(1LL, units);
-  return (int)std::max(1LL, std::min(std::min(want, tiles / 4), 64LL));
+// How the keys are cut: enough pieces that `units` CTAs a piece fill `ctas`, none under 4 tiles.
+int pieces_for(long long units, long long ctas, long long tiles) {
+  const long long want = ctas / std::max(1LL, units);
+  return (int)std::max(1LL, std::min(std::min(want, (tiles + 3) / 4), 64LL));
 }
 
+// Which kernel does which part.
 struct PrefixPlan {
-  int rg, tiles1, tiles2, ns1, ns2;
+  int rg;                  // rows of a CUDA-core tile
+  int simt1, simt2;        // its row tiles: packed (prefix), of a request (own keys); 0: not its part
+  int tc1, tc2;            // 256-row tiles on the tensor cores, the same way
+  bool fused, direct;      // request tiles take the prefix too; one piece in all, no merge
+  int ns1, ns2;
   size_t ml_bytes, o_bytes;
 };
 
-PrefixPlan plan_of(int T, int B, int Hq, int Hk, int d, int page, int table_ld, int prefix_len,
-                   int max_q) {
-  PrefixPlan w;
+PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, int table_ld,
+                   int prefix_len, int max_q) {
+  PrefixPlan w = {};
   const int G = Hq / Hk;
-  w.rg = (long long)max_q * G <= 16 ? 16 : 64;
-  const long long rows = (long long)T * G;
-  w.tiles1 = (int)((rows + w.rg - 1) / w.rg);
-  w.tiles2 = (int)(((long long)max_q * G + w.rg - 1) / w.rg);
+  const long long rows = (long long)T * G, rows_q = (long long)max_q * G;
   const long long keys2 = (long long)table_ld * page;
-  w.ns1 = prefix_len ? pieces_for((long long)w.tiles1 * Hk, (prefix_len + 63) / 64) : 0;
-  w.ns2 = keys2 ? pieces_for((long long)w.tiles2 * B * Hk, (keys2 + 63) / 64) : 0;
-  const long long all = (long long)T * Hq * (w.ns1 + w.ns2);
+  w.rg = rows_q <= 16 ? 16 : 64;
+  auto tiles = [](long long n, int of) { return (int)((n + of - 1) / of); };
+  // The tensor cores pad a tile to 128 rows: they take the packed rows from 17 on (below, a CUDA-core
+  // tile of 16 rows holds them all) and a request's own keys when it has more than 16 rows.
+  if (dt == BSA_BF16 && rows_q > 16) {
+    // Requests that fill half a 128-row tile on average keep their rows to themselves: prefix and
+    // own keys in one pass.  Below that the padding would cost more than the merge.
+    w.fused = rows >= 64LL * B;
+    w.tc2 = tiles(rows_q, 256);
+    if (!w.fused && prefix_len) w.tc1 = tiles(rows, 256);
+  } else {
+    if (dt == BSA_BF16 && rows > 16) w.tc1 = prefix_len ? tiles(rows, 256) : 0;
+    else w.simt1 = prefix_len ? tiles(rows, w.rg) : 0;
+    w.simt2 = keys2 ? tiles(rows_q, w.rg) : 0;
+  }
+  if (w.tc1) w.ns1 = pieces_for((long long)w.tc1 * Hk, kSMs, (prefix_len + 127) / 128);
+  if (w.simt1) w.ns1 = pieces_for((long long)w.simt1 * Hk, 2 * kSMs, (prefix_len + 63) / 64);
+  if (w.tc2)
+    w.ns2 = pieces_for((rows + 255) / 256 * Hk, kSMs,
+                       (keys2 + (w.fused ? prefix_len : 0) + 127) / 128);
+  if (w.simt2) w.ns2 = pieces_for((long long)w.simt2 * B * Hk, 2 * kSMs, (keys2 + 63) / 64);
+  w.direct = w.tc2 && !w.tc1 && w.ns2 == 1;
+  const long long all = w.direct ? 0 : (long long)T * Hq * (w.ns1 + w.ns2);
   w.ml_bytes = align_up((size_t)all * sizeof(float2), 256);
   w.o_bytes = (size_t)all * d * sizeof(float);
   return w;
@@ -313,19 +335,32 @@ PrefixPlan plan_of(int T, int B, int Hq, int Hk, int d, int page, int table_ld, 
 
 template <typename T, int D, int RG>
 bsa_status launch_simt(const PrefixParams& p, const PrefixPlan& w, cudaStream_t st) {
-  const long long units1 = p.ns1 ? (long long)w.tiles1 * p.Hk * p.ns1 : 0;
-  const long long units2 = (long long)p.B * w.tiles2 * p.Hk * p.ns2;
+  const long long units1 = (long long)w.simt1 * p.Hk * p.ns1;
+  const long long units2 = (long long)p.B * w.simt2 * p.Hk * p.ns2;
   if (units1 + units2 > INT_MAX) return BSA_ERR_UNSUPPORTED;
-  if (units1 + units2 > 0) {
-    auto kern = prefix_simt_kernel<T, D, RG>;
-    const int smem = SimtSmem<D, RG>::kTotal;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-        cudaSuccess) {
-      (void)cudaGetLastError();
-      return BSA_ERR_CUDA;
-    }
-    kern<<<(int)(units1 + units2), kPsThreads, smem, st>>>(p, SimtGrid{(int)units1, w.tiles2});
-    BSA_LAUNCH_CHECK();
+  if (units1 + units2 == 0) return BSA_OK;
+  auto kern = prefix_simt_kernel<T, D, RG>;
+  const int smem = SimtSmem<D, RG>::kTotal;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return BSA_ERR_CUDA;
+  }
+  kern<<<(int)(units1 + units2), kPsThreads, smem, st>>>(p, SimtGrid{(int)units1, w.simt2});
+  BSA_LAUNCH_CHECK();
+  return BSA_OK;
+}
+
+template <typename T, int D>
+bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status, cudaStream_t st) {
+  if constexpr (sizeof(T) == 2) {
+    const bsa_status rc = prefix_attn_tc(p, D, w.tc1, w.tc2, w.fused, w.direct, status, st);
+    if (rc != BSA_OK || w.direct) return rc;
+  }
+  if (w.simt1 || w.simt2) {
+    const bsa_status rc =
+        w.rg == 16 ? launch_simt<T, D, 16>(p, w, st) : launch_simt<T, D, 64>(p, w, st);
+    if (rc != BSA_OK) return rc;
   }
   const long long rows = (long long)p.T * p.Hq;
   prefix_merge_kernel<T, D><<<(int)((rows + 7) / 8), 256, 0, st>>>(p);
@@ -352,7 +387,7 @@ extern "C" size_t bsa_prefix_attn_workspace_bytes(bsa_dtype dt, int T, int B, in
   if (!dtype_ok(dt) || !sizes_ok(T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q) ||
       !head_dim_ok(d) || !group_ok(Hq, Hk) || !page_ok(page))
     return 0;
-  const PrefixPlan w = plan_of(T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q);
+  const PrefixPlan w = plan_of(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q);
   return w.ml_bytes + w.o_bytes;
 }
 
@@ -361,8 +396,8 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
                                       int Hk, int d, int page, int num_pages, const int* table,
                                       int table_ld, const int* lens, const int* prefix_table,
                                       int prefix_len, const int* cu_q, int max_q, void* o,
-                                      float* lse, void* workspace, size_t workspace_bytes,
-                                      void* stream) {
+                                      float* lse, int* status, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
   BSA_REQUIRE(sizes_ok(T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q) && num_pages >= 1,
               BSA_ERR_ARG);
   BSA_REQUIRE(dtype_ok(dt), BSA_ERR_DTYPE);
@@ -381,7 +416,7 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
   BSA_REQUIRE(all_aligned16(q, k_pages, v_pages, o) && (T <= 1 || q_stride * es % 16 == 0),
               BSA_ERR_ARG);
   if (T == 0 || B == 0) return BSA_OK;
-  const PrefixPlan w = plan_of(T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q);
+  const PrefixPlan w = plan_of(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q);
   const size_t need = w.ml_bytes + w.o_bytes;
   BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), BSA_ERR_WORKSPACE);
   BSA_REQUIRE(aligned16(workspace), BSA_ERR_ARG);
@@ -399,14 +434,9 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.ml_bytes);
   p.ns1 = w.ns1; p.ns2 = w.ns2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  auto go = [&](auto type, auto dim) {
-    using E = decltype(type);
-    constexpr int D = decltype(dim)::value;
-    return w.rg == 16 ? launch_simt<E, D, 16>(p, w, st) : launch_simt<E, D, 64>(p, w, st);
-  };
-  using D64 = std::integral_constant<int, 64>;
-  using D128 = std::integral_constant<int, 128>;
   if (dt == BSA_BF16)
-    return d == 64 ? go(__nv_bfloat16(), D64()) : go(__nv_bfloat16(), D128());
-  return d == 64 ? go(float(), D64()) : go(float(), D128());
+    return d == 64 ? launch_parts<__nv_bfloat16, 64>(p, w, status, st)
+                   : launch_parts<__nv_bfloat16, 128>(p, w, status, st);
+  return d == 64 ? launch_parts<float, 64>(p, w, status, st)
+                 : launch_parts<float, 128>(p, w, status, st);
 }

@@ -52,4 +52,8 @@ __device__ __forceinline__ int pa_tokens(const PrefixParams& p) {
   return p.cu_q ? min(max(p.cu_q[p.B], 0), p.T) : p.B;
 }
 
+// prefix_attn_tc.cu
+bsa_status prefix_attn_tc(const PrefixParams& p, int d, int tiles1, int tiles2, bool fused,
+                          bool direct, int* status, cudaStream_t st);
+
 }  // namespace bsa

@@ -1,0 +1,626 @@
+// bsa_prefix_attn on the tensor cores (bf16): 128-row query tiles, tcgen05 with S, P and O in TMEM.
+//
+// A unit is up to 256 rows of one kv head (row = token * G + head of the group, so one TMA box over
+// a (d, G, Hk, T) view of q is a query tile) and a piece of their keys, in tiles of 128.  Rows are
+//   packed:  the tokens of ALL requests one after another, against the prefix: its keys are read
+//            once per 256 rows whatever the number of requests;
+//   request: one request's tokens against its own pages (causal) or, when a request fills tiles by
+//            itself, against prefix and own pages in one pass, with nothing to merge.
+// One CTA per SM runs two softmax streams, each with its own S / P / O in TMEM (128 + D columns) and
+// a warpgroup: while one stream's softmax runs, the tensor cores do the other's products.
+//   wide (more than 128 rows):  stream s owns rows 128 s ..; both read every key tile;
+//   deep (up to 128 rows):      both own the same rows and take alternate key tiles; the two halves
+//                               are joined at the end.  Keys in flight and softmax rate stay the same.
+// A tile of 128 x 128 scores needs 16,384 exponentials (1,024 clocks of the SM's 16 per clock) against
+// 512 clocks of tensor work at d = 128: long units are bound by the exponentials and the FMAs around
+// them, short batches (packed rows up to about 256) by HBM.
+//   warps 0-3, 4-7: softmax of stream 0, 1 (a thread owns a row: TMEM lane = row)
+//   warp 8: TMA producer; lane i loads box i (a page, or 128 rows of one) of K and V into a ring
+//   warp 9: MMA issuer (lane 0); all its lanes zero the V rows behind the last key, because
+//           0 x NaN of a place never written would reach the row
+//   warps 10, 11: none (they complete the helper warpgroup, whose registers the softmax takes)
+// P is written over S in TMEM and read from there as the A operand.  S_s of step i + 1 is issued
+// behind P V_s of step i, so its completion also says that O_s may be rescaled (lazily: only when a
+// row's maximum rises by more than 2^8, else the old maximum stays and P just exceeds 1).
+// Every mbarrier wait is bounded; a role whose wait runs out stops, the unit's rows get sum NaN, and
+// the CTA reaches its last barrier and frees TMEM.
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "prefix_attn.cuh"
+#include "tc_common.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kXThreads = 384;
+// registers: 168 a thread at launch, moved from the helper warpgroup to the softmax warpgroups, which
+// hold a row of 128 scores (2 x 216 + 72 = 3 x 168)
+constexpr int kXRegsSoftmax = 216, kXRegsHelper = 72;
+constexpr int kXKeys = 128;
+constexpr float kXRescale = 8.f;  // log2 units
+constexpr int kXMasks = 8;        // key tiles whose page masks are kept: more than the ring holds
+
+template <int D>
+struct TcSmem {
+  static constexpr int kTile = 128 * D * 2;  // 128 rows: [D / 64][128 x 128 B], 128-byte swizzle
+  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kTotal = kRing + kSlots * kTile;
+};
+
+struct TcGrid {
+  int units1;   // CTAs over packed rows
+  int tiles1;   // 256-row tiles of the packed rows
+  int tiles2;   // of a request
+  int fused;    // request units take the prefix too
+  int direct;   // one piece in all: o and lse are written here
+  int boxes;    // boxes of a key tile (128 / rows of a box)
+  int box_shift;
+  int* status;
+};
+
+// D[tmem] (+)= A[tmem] x B[smem desc]
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
+                                            int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// What a CTA works on.
+struct Unit {
+  int t0, r0;        // first token; first row among the packed rows (t0 * G)
+  int nrows, h, slot;
+  int n0, n1;        // keys of the prefix and of the request's own pages
+  int tiles0;        // key tiles of the prefix; the own ones follow
+  const int* own;    // own pages
+  int first_pos;     // row r sees own keys j <= first_pos + r / G
+  int tile0, tile1;  // the piece
+};
+
+__device__ __forceinline__ Unit unit_of(const PrefixParams& p, const TcGrid& g) {
+  Unit u;
+  int i = blockIdx.x, piece, pieces;
+  if (i < g.units1) {
+    piece = i % p.ns1;
+    i /= p.ns1;
+    const int tile = i % g.tiles1;
+    u.h = i / g.tiles1;
+    u.r0 = tile * 256;
+    u.t0 = u.r0 / p.G;
+    u.nrows = min(256, pa_tokens(p) * p.G - u.r0);
+    u.n0 = p.prefix_len;
+    u.n1 = 0;
+    u.own = nullptr;
+    u.first_pos = -1;
+    u.slot = piece;
+    pieces = p.ns1;
+  } else {
+    // kv head slowest: the CTAs that run together read the same keys
+    i -= g.units1;
+    piece = i % p.ns2;
+    i /= p.ns2;
+    const int tile = i % g.tiles2;
+    i /= g.tiles2;
+    const int b = i % p.B;
+    u.h = i / p.B;
+    const PaRequest r = pa_request(p, b);
+    u.t0 = r.t0 + tile * (256 / p.G);
+    u.r0 = u.t0 * p.G;
+    u.nrows = min(256, min(r.nq, p.max_q) * p.G - tile * 256);
+    u.first_pos = r.len - r.nq + tile * (256 / p.G);
+    u.n0 = g.fused ? p.prefix_len : 0;
+    u.n1 = max(0, min(r.len, u.first_pos + (u.nrows - 1) / p.G + 1));
+    u.own = p.table + (size_t)b * p.table_ld;
+    u.slot = p.ns1 + piece;
+    pieces = p.ns2;
+  }
+  u.tiles0 = (u.n0 + kXKeys - 1) / kXKeys;
+  const int tiles = u.tiles0 + (u.n1 + kXKeys - 1) / kXKeys;
+  const int per = (tiles + pieces - 1) / pieces;
+  u.tile0 = min(piece * per, tiles);
+  u.tile1 = min(u.tile0 + per, tiles);
+  return u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kXThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap tmq,
+                     const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv, const PrefixParams p,
+                     const TcGrid g) {
+  using L = TcSmem<D>;
+  constexpr int kHalves = D / 64;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = smem_align1024(smem_raw);
+  __shared__ __align__(8) uint64_t bars[2 * L::kSlots + kXMasks + 7];
+  uint64_t* full = bars;
+  uint64_t* empty = full + L::kSlots;
+  uint64_t* mask_full = empty + L::kSlots;  // page mask of a key tile written
+  uint64_t* q_full = mask_full + kXMasks;
+  uint64_t* s_full = q_full + 1;  // [2]
+  uint64_t* p_full = s_full + 2;  // [2]
+  uint64_t* o_done = p_full + 2;  // [2]
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ uint32_t s_mask[kXMasks];  // boxes of the key tile that are on pages of the pool
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Unit u = unit_of(p, g);
+  if (u.nrows <= 0) return;
+  const long long rows = (long long)p.T * p.Hq;
+  auto row_id = [&](int r) {
+    const int rr = u.r0 + r;
+    return (long long)(rr / p.G) * p.Hq + u.h * p.G + rr % p.G;
+  };
+  if (u.tile0 >= u.tile1) {  // no key: rows of sum 0
+    for (int r = tid; r < u.nrows; r += kXThreads) {
+      if (g.direct) {
+        if (p.lse) p.lse[row_id(r)] = -INFINITY;
+        uint4* op = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row_id(r) * D);
+        for (int c = 0; c < D / 8; ++c) op[c] = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        p.part_ml[u.slot * rows + row_id(r)] = make_float2(-INFINITY, 0.f);
+      }
+    }
+    return;
+  }
+  const bool wide = u.nrows > 128;
+  const int nt = u.tile1 - u.tile0;
+  // steps of stream s and the tile of a step
+  auto steps = [&](int s) { return wide ? nt : (nt - s + 1) >> 1; };
+  auto tile_at = [&](int s, int i) { return wide ? i : 2 * i + s; };
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kXMasks; ++i) mbar_init(&mask_full[i], 1);
+    mbar_init(q_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 128);
+      mbar_init(&o_done[s], 1);
+    }
+    fence_mbar_init();
+    s_abort = 0;
+  }
+  if (warp == 9) {
+    tc::tmem_alloc(&s_tmem, 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    tc::prefetch_tmap(&tmq);
+    tc::prefetch_tmap(&tmk);
+    tc::prefetch_tmap(&tmv);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  auto s_col = [&](int s) { return tmem + (uint32_t)(s * 128); };
+  auto o_col = [&](int s) { return tmem + 256u + (uint32_t)(s * 128); };
+  auto slot_at = [&](int i) { return smem + L::kRing + i * L::kTile; };
+  const uint32_t all_boxes = (1u << g.boxes) - 1u;
+
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kXRegsHelper));
+  if (warp == 8) {
+    // ------------------------------------------------------------------------- producer
+    if (lane == 0) {
+      mbar_arrive_expect_tx(q_full, (wide ? 2 : 1) * L::kTile);
+      for (int s = 0; s < (wide ? 2 : 1); ++s)
+        for (int hf = 0; hf < kHalves; ++hf)
+          tma_load_4d(smem + L::kQ + s * L::kTile + hf * 16384, &tmq, hf * 64, 0, u.h,
+                      u.t0 + s * (128 / p.G), q_full);
+    }
+    // the page of lane's box in tile t, -1: nothing to load
+    auto page_of = [&](int t) -> int {
+      if (t >= u.tile1 || lane >= g.boxes) return -1;
+      const bool own = t >= u.tiles0;
+      const int j = (own ? t - u.tiles0 : t) * kXKeys + (lane << g.box_shift);
+      if (j >= (own ? u.n1 : u.n0)) return -1;
+      const int id = (own ? u.own : p.ptable)[j >> p.page_shift];
+      return id >= 0 && id < p.num_pages ? id : -1;
+    };
+    const uint32_t box_bytes = (uint32_t)(128 << g.box_shift);  // of one 64-column half
+    int next = page_of(u.tile0);
+    int k = 0;  // ring position
+    bool ok = true;
+    for (int i = 0; i < nt && ok; ++i) {
+      const int t = u.tile0 + i, id = next;
+      next = page_of(t + 1);
+      const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
+      // a box is one page: a page never exceeds the tile's 128 rows
+      const int y = ((id * p.Hk + u.h) << p.page_shift);
+      if (lane == 0) {
+        s_mask[i % kXMasks] = have;
+        mbar_arrive(&mask_full[i % kXMasks]);
+      }
+      for (int kv = 0; kv < 2; ++kv, ++k) {
+        const int sl = k % L::kSlots;
+        if (k >= L::kSlots) ok = mbar_wait_bounded(&empty[sl], ((k / L::kSlots) - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full[sl], (uint32_t)__popc(have) * box_bytes * kHalves);
+        __syncwarp();
+        if (id >= 0)
+          for (int hf = 0; hf < kHalves; ++hf)
+            tc::tma_load_2d(slot_at(sl) + hf * 16384 + lane * box_bytes, kv ? &tmv : &tmk, hf * 64,
+                            y, &full[sl]);
+      }
+    }
+    if (!ok && lane == 0) s_abort = 1;
+    // copies still in flight land before the CTA leaves, whatever the other roles do
+    for (int j = max(0, k - L::kSlots); j < k; ++j)
+      (void)mbar_wait_bounded(&full[j % L::kSlots], (j / L::kSlots) & 1);
+  } else if (warp == 9) {
+    // ----------------------------------------------------------------------- MMA issuer
+    constexpr uint32_t idS = tc::idesc_bf16(128, 128, false, false);
+    constexpr uint32_t idO = tc::idesc_bf16(128, D, false, true);
+    auto ready = [&](int k) {
+      return __all_sync(0xffffffffu,
+                        mbar_wait_bounded(&full[k % L::kSlots], (k / L::kSlots) & 1));
+    };
+    // S_s of the stream's step i
+    auto issue_s = [&](int s, int i) -> bool {
+      const int k = 2 * tile_at(s, i);
+      if (!ready(k)) return false;
+      if (lane == 0) {
+        tc::fence_after_sync();
+        const unsigned char* q = smem + L::kQ + (wide ? s : 0) * L::kTile;
+        const unsigned char* kt = slot_at(k % L::kSlots);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int at = (kk >> 2) * 16384 + (kk & 3) * 32;
+          tc::mma_f16_ss(s_col(s), tc::smem_desc_sw128(q + at, 16, 1024),
+                         tc::smem_desc_sw128(kt + at, 16, 1024), idS, kk > 0);
+        }
+        tc::mma_commit(&s_full[s]);
+        if (!wide || s == 1) tc::mma_commit(&empty[k % L::kSlots]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_full, 0));
+    for (int s = 0; s < 2 && ok; ++s)
+      if (steps(s) > 0) ok = issue_s(s, 0);
+    for (int i = 0; i < steps(0) && ok; ++i) {
+      for (int s = 0; s < 2 && ok; ++s) {
+        if (i >= steps(s)) continue;
+        const int ti = tile_at(s, i), k = 2 * ti + 1;
+        ok = ready(k);
+        if (!ok) break;
+        // rows of V without a key, once per tile
+        if (!wide || s == 0) {
+          const int t = u.tile0 + ti;
+          const bool own = t >= u.tiles0;
+          const int left = (own ? u.n1 : u.n0) - (own ? t - u.tiles0 : t) * kXKeys;
+          const uint32_t have = s_mask[ti % kXMasks];
+          if (left < kXKeys || have != all_boxes) {
+            unsigned char* vt = slot_at(k % L::kSlots);
+            for (int r = lane; r < kXKeys; r += 32) {
+              if (r < left && ((have >> (r >> g.box_shift)) & 1)) continue;
+              for (int hf = 0; hf < kHalves; ++hf)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  *reinterpret_cast<uint4*>(vt + hf * 16384 + r * 128 + c * 16) =
+                      make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async();
+            __syncwarp();
+          }
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&p_full[s], i & 1));
+        if (!ok) break;
+        if (lane == 0) {
+          tc::fence_after_sync();
+          const unsigned char* vt = slot_at(k % L::kSlots);
+#pragma unroll
+          for (int kk = 0; kk < kXKeys / 16; ++kk)
+            mma_f16_ts(o_col(s), s_col(s) + kk * 8,
+                       tc::smem_desc_sw128(vt + kk * 2048, 16384, 1024), idO,
+                       (i > 0 || kk > 0) ? 1u : 0u);
+          if (!wide || s == 1) tc::mma_commit(&empty[k % L::kSlots]);
+          if (i + 1 == steps(s)) tc::mma_commit(&o_done[s]);
+        }
+        __syncwarp();
+        if (i + 1 < steps(s)) ok = issue_s(s, i + 1);
+      }
+    }
+    if (!ok && lane == 0) s_abort = 1;
+    // every MMA issued has completed before TMEM and shared memory are given up
+    if (lane == 0 && !ok) {
+      tc::mma_commit(q_full);
+      (void)mbar_wait_bounded(q_full, 1);
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kXRegsSoftmax));
+    // ---------------------------------------------------------------- softmax of stream s
+    const int s = warp >> 2, r = (warp & 3) * 32 + lane;  // row of the stream's tile
+    const int row = r + (wide ? 128 * s : 0);             // row of the unit
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const float scale = rsqrtf((float)D) * kPaLog2e;
+    const int pos = u.first_pos + row / p.G;
+    const int ns = steps(s);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int i = 0; i < ns; ++i) {
+      const int ti = tile_at(s, i), t = u.tile0 + ti;
+      ok = mbar_wait_bounded(&mask_full[ti % kXMasks], (ti / kXMasks) & 1) &&
+           mbar_wait_bounded(&s_full[s], i & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t have = s_mask[ti % kXMasks];
+      float x[128];
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) tc::tmem_ld32(s_col(s) + lanes + c, x + c);
+      tc::tmem_wait_ld();
+      tc::reg_fence(x);
+      // columns of the tile the row sees: [0, hi), on pages of the pool
+      const bool own = t >= u.tiles0;
+      const int j0 = (own ? t - u.tiles0 : t) * kXKeys;
+      const int hi = (own ? min(u.n1, pos + 1) : u.n0) - j0;
+      if (!__all_sync(0xffffffffu, hi >= kXKeys && have == all_boxes)) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int left = hi - 32 * w;
+          uint32_t keep = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+          if (have != all_boxes) {
+            uint32_t on = 0;
+            for (int c = 0; c < 32; c += 16)
+              if ((have >> ((32 * w + c) >> g.box_shift)) & 1) on |= 0xffffu << c;
+            keep &= on;
+          }
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[32 * w + c] = (keep >> c) & 1 ? x[32 * w + c] : -INFINITY;
+        }
+      }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int c = 4; c < 124; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[c + e], x[c + 4 + e]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
+      const float m_new = fmaxf(m, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale);
+      const bool rescale = m != -INFINITY && m_new > m + kXRescale;
+      float corr = 1.f;
+      if (rescale) corr = tc::ex2_approx(m - m_new);
+      if (rescale || m == -INFINITY) m = m_new;
+      if (i > 0 && __any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float ov[32];
+          tc::tmem_ld32(o_col(s) + lanes + c, ov);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] *= corr;
+          tc::tmem_st32(o_col(s) + lanes + c, ov);
+        }
+      }
+      const float neg_m = m == -INFINITY ? 0.f : -m;  // hidden keys give 2^-inf = 0
+      const uint64_t sc2 = tc::pack_f2(scale, scale), nm2 = tc::pack_f2(neg_m, neg_m);
+      uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float a0, a1;
+          tc::unpack_f2(tc::fma_f2(tc::pack_f2(x[c + e], x[c + e + 1]), sc2, nm2), a0, a1);
+          const float p0 = tc::ex2_approx(a0), p1 = tc::ex2_approx(a1);
+          sum2[(e >> 1) & 3] = tc::add_f2(sum2[(e >> 1) & 3], tc::pack_f2(p0, p1));
+          // weights are rounded to bf16 for the product with V; their sum is not
+          const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+          pk[e / 2] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
+        tmem_st16(s_col(s) + lanes + c / 2, pk);
+      }
+      float sl[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tc::unpack_f2(sum2[e], sl[2 * e], sl[2 * e + 1]);
+      l = l * corr + (((sl[0] + sl[1]) + (sl[2] + sl[3])) + ((sl[4] + sl[5]) + (sl[6] + sl[7])));
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      mbar_arrive(&p_full[s]);
+    }
+    if (ok && ns > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&o_done[s], 0));
+    if (!ok) {
+      s_abort = 1;
+      m = 0.f;
+      l = NAN;
+    }
+    tc::fence_after_sync();
+    // deep units: the second stream's half joins through shared memory (the ring: both
+    // streams' products are complete behind the first barrier)
+    float w = 1.f;
+    unsigned char* xch = smem + L::kRing;
+    auto at = [&](int c4) { return xch + (r * (D / 4) + (c4 ^ (r & (D / 4 - 1)))) * 16; };
+    if (!wide) {
+      float2* ml = reinterpret_cast<float2*>(smem + L::kQ + L::kTile);  // no second query tile
+      ml[s * 128 + r] = make_float2(m, l);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float2 other = ml[(s ^ 1) * 128 + r];
+      const float top = fmaxf(m, other.x);
+      const float base = top == -INFINITY ? 0.f : top;
+      w = tc::ex2_approx(m - base);
+      if (s == 1 && ns > 0) {
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float ov[32];
+          tc::tmem_ld32(o_col(1) + lanes + c, ov);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(at((c + e) / 4)) =
+                make_float4(ov[e] * w, ov[e + 1] * w, ov[e + 2] * w, ov[e + 3] * w);
+        }
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      l = l * w + other.y * tc::ex2_approx(other.x - base);
+      m = top;
+    }
+    if (wide || s == 0) {
+      const bool join = !wide && nt > 1;
+      const bool live = row < u.nrows;
+      const long long id = live ? row_id(row) : 0;
+      const float inv = !g.direct ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      if (live) {
+        if (!g.direct) p.part_ml[u.slot * rows + id] = make_float2(m, l);
+        else if (p.lse) p.lse[id] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPaLn2;
+      }
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        float ov[32];
+        tc::tmem_ld32(o_col(s) + lanes + c, ov);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          float4 o4 = make_float4(ov[e] * w, ov[e + 1] * w, ov[e + 2] * w, ov[e + 3] * w);
+          if (join) {
+            const float4 x4 = *reinterpret_cast<const float4*>(at((c + e) / 4));
+            o4 = make_float4(o4.x + x4.x, o4.y + x4.y, o4.z + x4.z, o4.w + x4.w);
+          }
+          ov[e] = o4.x; ov[e + 1] = o4.y; ov[e + 2] = o4.z; ov[e + 3] = o4.w;
+        }
+        if (!live) continue;
+        if (g.direct) {
+          __nv_bfloat16* op = static_cast<__nv_bfloat16*>(p.o) + id * D + c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            __nv_bfloat162 b2[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f)  // a row without a key: 0, not what TMEM holds
+              b2[f] = __floats2bfloat162_rn(l == 0.f ? 0.f : ov[e + 2 * f] * inv,
+                                            l == 0.f ? 0.f : ov[e + 2 * f + 1] * inv);
+            *reinterpret_cast<uint4*>(op + e) = *reinterpret_cast<uint4*>(b2);
+          }
+        } else {
+          float* op = p.part_o + (u.slot * rows + id) * D + c;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(op + e) =
+                make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (s_abort && tid == 0) report_timeout(g.status, 5);
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    else
+      (void)cudaGetLastError();
+  });
+  return fn;
+}
+
+template <int D>
+bsa_status launch_tc(const PrefixParams& p, const TcGrid& g, int grid, cudaStream_t st) {
+  CUtensorMap tmq, tmk, tmv;
+  auto enc = encode_fn();
+  if (!enc) return BSA_ERR_CUDA;
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  {
+    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.G, (cuuint64_t)p.Hk, (cuuint64_t)p.T};
+    cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)p.G * D * 2,
+                             (cuuint64_t)p.q_stride * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)p.G, 1, (cuuint32_t)(128 / p.G)};
+    if (enc(&tmq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.q), dims, strides, box,
+            ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return BSA_ERR_CUDA;
+  }
+  for (int kv = 0; kv < 2; ++kv) {
+    cuuint64_t dims[2] = {(cuuint64_t)D, ((cuuint64_t)p.num_pages * p.Hk) << p.page_shift};
+    cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)1 << g.box_shift};
+    if (enc(kv ? &tmv : &tmk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(kv ? p.v : p.k), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return BSA_ERR_CUDA;
+  }
+  const int smem = TcSmem<D>::kTotal + 1024;  // + alignment slack
+  auto kern = prefix_tc_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return BSA_ERR_CUDA;
+  }
+  kern<<<grid, kXThreads, smem, st>>>(tmq, tmk, tmv, p, g);
+  BSA_LAUNCH_CHECK();
+  return BSA_OK;
+}
+
+}  // namespace
+
+// The units of a plan on the tensor cores: packed rows x prefix (tiles1 > 0, p.ns1 pieces) and
+// requests x own keys (tiles2 > 0, p.ns2 pieces; `fused`: prefix and own keys).
+bsa_status prefix_attn_tc(const PrefixParams& p, int d, int tiles1, int tiles2, bool fused,
+                          bool direct, int* status, cudaStream_t st) {
+  TcGrid g;
+  const long long units1 = (long long)tiles1 * p.Hk * p.ns1;
+  const long long units2 = (long long)tiles2 * p.B * p.Hk * p.ns2;
+  if (units1 + units2 > INT_MAX) return BSA_ERR_UNSUPPORTED;
+  if (units1 + units2 == 0) return BSA_OK;
+  g.units1 = (int)units1;
+  g.tiles1 = tiles1;
+  g.tiles2 = tiles2;
+  g.fused = fused;
+  g.direct = direct;
+  g.box_shift = p.page_shift;
+  g.boxes = kXKeys >> p.page_shift;
+  g.status = status;
+  const int grid = (int)(units1 + units2);
+  return d == 64 ? launch_tc<64>(p, g, grid, st) : launch_tc<128>(p, g, grid, st);
+}
+
+}  // namespace bsa

@@ -574,6 +574,8 @@ bsa_status bsa_paged_append(const void* k, const void* v, bsa_dtype dt, int T, i
  *   o [T, Hq, d] out; lse [T, Hq] optional out.  A token that sees no key gets o = 0, lse = -inf.
  *             Rows at or after cu_q[B], and tokens beyond the max_q-th of a request, are left as
  *             they were.
+ *   status    optional device int: a bounded wait that runs out writes a nonzero value there (and
+ *             the rows it concerns become NaN).
  *   workspace device scratch of bsa_prefix_attn_workspace_bytes() bytes, 16-byte aligned; needs no
  *             initialisation and may be reused once the stream has passed the call.  Calls that
  *             share one must not run at the same time.
@@ -586,8 +588,8 @@ bsa_status bsa_prefix_attn(const void* q, long long q_stride, const void* k_page
                            const void* v_pages, bsa_dtype dt, int T, int B, int Hq, int Hk, int d,
                            int page, int num_pages, const int* table, int table_ld,
                            const int* lens, const int* prefix_table, int prefix_len,
-                           const int* cu_q, int max_q, void* o, float* lse, void* workspace,
-                           size_t workspace_bytes, void* stream);
+                           const int* cu_q, int max_q, void* o, float* lse, int* status,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes bsa_prefix_attn needs for these sizes (0 for unsupported ones). */
 size_t bsa_prefix_attn_workspace_bytes(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page,

@@ -53,7 +53,7 @@ def test_paged_append_refusals(bsa_lib, change, code):
 
 ATTN = dict(q=FAKE, q_stride=1024, k=FAKE, v=FAKE, dt=1, T=4, B=4, Hq=8, Hk=2, d=128, page=64,
             num_pages=64, table=FAKE, ld=8, lens=FAKE, ptable=FAKE, prefix=100, cu_q=None, max_q=1,
-            o=FAKE, lse=None, ws=FAKE, ws_bytes=0, stream=None)
+            o=FAKE, lse=None, status=None, ws=FAKE, ws_bytes=0, stream=None)
 
 
 @pytest.mark.parametrize("change,code", [

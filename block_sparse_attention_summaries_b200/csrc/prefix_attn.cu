@@ -238,11 +238,12 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p)
   const long long rows = (long long)p.T * p.Hq;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rows) return;
-  const int t = (int)(row / p.Hq);
+  const int t = (int)(row / p.Hq), hq = (int)(row - (long long)t * p.Hq);
   if (t >= pa_tokens(p)) return;
+  int b = t;
   if (p.cu_q) {
     // the request of the token: how many requests end at or before it
-    int b = 0;
+    b = 0;
     for (int i = 0; i < p.B; i += 32) {
       const bool before = i + lane < p.B && p.cu_q[i + lane + 1] <= t;
       b += __popc(__ballot_sync(0xffffffffu, before));
@@ -250,22 +251,69 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p)
     // tokens beyond max_q of their request were not attended
     if (b >= p.B || t - p.cu_q[b] >= p.max_q) return;
   }
-  const int ns = p.ns1 + p.ns2;
+  // the row's pieces: dense ones, then up to two runs of item slots
+  int first[2] = {0, 0}, count[2] = {0, 0}, at[2] = {0, 0};
+  if (p.item_ctas) {
+    const int h = hq / p.G, g = hq - h * p.G;
+    auto pieces = [&](int k, int item, int r) {
+      const int2 c = p.item_cta[item];  // cut: a run that stopped early has not written it
+      const int c0 = min(max(c.x, 0), p.item_ctas - 1), c1 = min(max(c.y, c0), p.item_ctas - 1);
+      first[k] = item + c0;
+      count[k] = c1 - c0 + 1;
+      at[k] = r;
+    };
+    if (p.prefix_items) pieces(0, h, t * p.G + g);
+    const PaRequest r = pa_request(p, b);
+    if (pa_own_keys(p, r) > 0) pieces(1, p.prefix_items + b * p.Hk + h, (t - r.t0) * p.G + g);
+  }
+  const int ns = p.ns1 + p.ns2, n = ns + count[0] + count[1];
+  auto piece = [&](int s, const float2*& ml, const float*& o) {
+    if (s < ns) {
+      const long long i = s * rows + row;
+      ml = p.part_ml + i;
+      o = p.part_o + i * D;
+    } else {
+      const int k = s - ns < count[0] ? 0 : 1;
+      const long long i =
+          (long long)(first[k] + s - ns - (k ? count[0] : 0)) * p.item_rows + at[k];
+      ml = p.item_ml + i;
+      o = p.item_o + i * D;
+    }
+  };
   float top = -INFINITY;
-  for (int s = lane; s < ns; s += 32) top = fmaxf(top, p.part_ml[s * rows + row].x);
+  for (int s = lane; s < n; s += 32) {
+    const float2* ml;
+    const float* o;
+    piece(s, ml, o);
+    top = fmaxf(top, ml->x);
+  }
   top = warp_max(top);
   float acc[C], l = 0.f;
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
-  for (int s = 0; s < ns; ++s) {
-    const float2 ml = p.part_ml[s * rows + row];
-    if (ml.y == 0.f) continue;
-    const float w = exp2f(ml.x - top);
-    float x[C];
-    load_vec<float, C>(p.part_o + (s * rows + row) * D + lane * C, x);
-    l += ml.y * w;
+  constexpr int kAhead = 4;  // pieces loaded together
+  for (int s0 = 0; s0 < n; s0 += kAhead) {
+    float2 ml[kAhead];
+    float x[kAhead][C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] += x[c] * w;
+    for (int e = 0; e < kAhead; ++e) {
+      ml[e] = make_float2(0.f, 0.f);
+      if (s0 + e < n) {
+        const float2* mp;
+        const float* op;
+        piece(s0 + e, mp, op);
+        ml[e] = *mp;
+        load_vec<float, C>(op + lane * C, x[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      if (ml[e].y == 0.f) continue;  // no key in the piece: its o was not written
+      const float w = exp2f(ml[e].x - top);
+      l += ml[e].y * w;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += x[e][c] * w;
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;  // no key at all: o = 0
   T* op = static_cast<T*>(p.o) + row * D + lane * C;
@@ -289,14 +337,19 @@ int pieces_for(long long units, long long ctas, long long tiles) {
   return (int)std::max(1LL, std::min(std::min(want, (tiles + 3) / 4), 64LL));
 }
 
+constexpr int kRowsCtas = 2 * kSMs;  // of the few-rows kernel: two per SM
+
 // Which kernel does which part.
 struct PrefixPlan {
   int rg;                  // rows of a CUDA-core tile
   int simt1, simt2;        // its row tiles: packed (prefix), of a request (own keys); 0: not its part
   int tc1, tc2;            // 256-row tiles on the tensor cores, the same way
   bool fused, direct;      // request tiles take the prefix too; one piece in all, no merge
-  int ns1, ns2;
-  size_t ml_bytes, o_bytes;
+  bool rows, rows_prefix;  // own keys (and the prefix) as items of the few-rows kernel
+  int ns1, ns2, item_rows;
+  long long items;
+  size_t ml_bytes, o_bytes, cta_bytes, item_ml_bytes, item_o_bytes;
+  size_t bytes() const { return ml_bytes + o_bytes + cta_bytes + item_ml_bytes + item_o_bytes; }
 };
 
 PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, int table_ld,
@@ -307,17 +360,23 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
   const long long keys2 = (long long)table_ld * page;
   w.rg = rows_q <= 16 ? 16 : 64;
   auto tiles = [](long long n, int of) { return (int)((n + of - 1) / of); };
-  // The tensor cores pad a tile to 128 rows: they take the packed rows from 17 on (below, a CUDA-core
-  // tile of 16 rows holds them all) and a request's own keys when it has more than 16 rows.
   if (dt == BSA_BF16 && rows_q > 16) {
-    // Requests that fill half a 128-row tile on average keep their rows to themselves: prefix and
-    // own keys in one pass.  Below that the padding would cost more than the merge.
+    // A request with more than 16 rows: 128-row tiles on the tensor cores.  Requests that fill half
+    // a tile on average keep their rows to themselves: prefix and own keys in one pass.  Below that
+    // the padding would cost more than the merge.
     w.fused = rows >= 64LL * B;
     w.tc2 = tiles(rows_q, 256);
     if (!w.fused && prefix_len) w.tc1 = tiles(rows, 256);
+  } else if (dt == BSA_BF16) {
+    // Up to 16 rows share a key: the few-rows kernel; it takes the prefix too while all rows of a kv
+    // head fit its 16, else they fill 128-row tiles.
+    w.rows = true;
+    w.rows_prefix = prefix_len && rows <= 16;
+    if (prefix_len && !w.rows_prefix) w.tc1 = tiles(rows, 256);
+    w.item_rows = (int)(w.rows_prefix ? std::max(rows, rows_q) : rows_q);
+    w.items = (w.rows_prefix ? Hk : 0) + (long long)B * Hk;
   } else {
-    if (dt == BSA_BF16 && rows > 16) w.tc1 = prefix_len ? tiles(rows, 256) : 0;
-    else w.simt1 = prefix_len ? tiles(rows, w.rg) : 0;
+    w.simt1 = prefix_len ? tiles(rows, w.rg) : 0;
     w.simt2 = keys2 ? tiles(rows_q, w.rg) : 0;
   }
   if (w.tc1) w.ns1 = pieces_for((long long)w.tc1 * Hk, kSMs, (prefix_len + 127) / 128);
@@ -329,7 +388,13 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
   w.direct = w.tc2 && !w.tc1 && w.ns2 == 1;
   const long long all = w.direct ? 0 : (long long)T * Hq * (w.ns1 + w.ns2);
   w.ml_bytes = align_up((size_t)all * sizeof(float2), 256);
-  w.o_bytes = (size_t)all * d * sizeof(float);
+  w.o_bytes = align_up((size_t)all * d * sizeof(float), 256);
+  if (w.rows) {
+    const size_t slots = (size_t)(w.items + kRowsCtas) * w.item_rows;
+    w.cta_bytes = align_up((size_t)w.items * sizeof(int2), 256);
+    w.item_ml_bytes = align_up(slots * sizeof(float2), 256);
+    w.item_o_bytes = slots * d * sizeof(float);
+  }
   return w;
 }
 
@@ -356,6 +421,10 @@ bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status,
   if constexpr (sizeof(T) == 2) {
     const bsa_status rc = prefix_attn_tc(p, D, w.tc1, w.tc2, w.fused, w.direct, status, st);
     if (rc != BSA_OK || w.direct) return rc;
+    if (w.rows) {
+      const bsa_status rr = prefix_attn_rows(p, D, w.rows_prefix, status, st);
+      if (rr != BSA_OK) return rr;
+    }
   }
   if (w.simt1 || w.simt2) {
     const bsa_status rc =
@@ -388,7 +457,7 @@ extern "C" size_t bsa_prefix_attn_workspace_bytes(bsa_dtype dt, int T, int B, in
       !head_dim_ok(d) || !group_ok(Hq, Hk) || !page_ok(page))
     return 0;
   const PrefixPlan w = plan_of(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q);
-  return w.ml_bytes + w.o_bytes;
+  return w.bytes();
 }
 
 extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const void* k_pages,
@@ -417,7 +486,7 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
               BSA_ERR_ARG);
   if (T == 0 || B == 0) return BSA_OK;
   const PrefixPlan w = plan_of(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q);
-  const size_t need = w.ml_bytes + w.o_bytes;
+  const size_t need = w.bytes();
   BSA_REQUIRE(need == 0 || (workspace && workspace_bytes >= need), BSA_ERR_WORKSPACE);
   BSA_REQUIRE(aligned16(workspace), BSA_ERR_ARG);
   PrefixParams p;
@@ -430,9 +499,17 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
   p.ptable = prefix_table; p.prefix_len = prefix_len;
   p.cu_q = cu_q; p.max_q = max_q;
   p.o = o; p.lse = lse;
-  p.part_ml = static_cast<float2*>(workspace);
-  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.ml_bytes);
+  BSA_REQUIRE(w.items <= INT_MAX - kRowsCtas, BSA_ERR_UNSUPPORTED);
+  char* ws = static_cast<char*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  p.part_o = reinterpret_cast<float*>(ws += w.ml_bytes);
+  p.item_cta = reinterpret_cast<int2*>(ws += w.o_bytes);
+  p.item_ml = reinterpret_cast<float2*>(ws += w.cta_bytes);
+  p.item_o = reinterpret_cast<float*>(ws += w.item_ml_bytes);
   p.ns1 = w.ns1; p.ns2 = w.ns2;
+  p.item_rows = w.item_rows;
+  p.item_ctas = w.rows ? kRowsCtas : 0;
+  p.prefix_items = w.rows_prefix ? Hk : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dt == BSA_BF16)
     return d == 64 ? launch_parts<__nv_bfloat16, 64>(p, w, status, st)

@@ -28,6 +28,13 @@ struct PrefixParams {
   float* part_o;
   float2* part_ml;
   int ns1, ns2;
+  // Pieces of prefix_attn_rows: item = kv head of the prefix (the first prefix_items), then request *
+  // Hk + kv head; item_cta[item] = first and last CTA that worked on it; the piece of CTA c is slot
+  // item + c of item_o [slot][item_rows][d] and item_ml [slot][item_rows].
+  int2* item_cta;
+  float* item_o;
+  float2* item_ml;
+  int item_rows, item_ctas, prefix_items;  // item_ctas = 0: no items
 };
 
 // Request b: its first new token, how many it has, its own tokens.  Values that would reach
@@ -47,6 +54,10 @@ __device__ __forceinline__ PaRequest pa_request(const PrefixParams& p, int b) {
   r.len = min(max(p.lens[b], 0), p.table_ld << p.page_shift);
   return r;
 }
+// Own keys of a request that any of its new tokens sees.
+__device__ __forceinline__ int pa_own_keys(const PrefixParams& p, const PaRequest& r) {
+  return r.nq > 0 ? max(0, r.len - r.nq + min(r.nq, p.max_q)) : 0;
+}
 // New tokens in all: rows at or after this are left as they were.
 __device__ __forceinline__ int pa_tokens(const PrefixParams& p) {
   return p.cu_q ? min(max(p.cu_q[p.B], 0), p.T) : p.B;
@@ -55,5 +66,9 @@ __device__ __forceinline__ int pa_tokens(const PrefixParams& p) {
 // prefix_attn_tc.cu
 bsa_status prefix_attn_tc(const PrefixParams& p, int d, int tiles1, int tiles2, bool fused,
                           bool direct, int* status, cudaStream_t st);
+
+// prefix_attn_rows.cu
+bsa_status prefix_attn_rows(const PrefixParams& p, int d, bool prefix, int* status,
+                            cudaStream_t st);
 
 }  // namespace bsa

@@ -574,8 +574,8 @@ bsa_status bsa_paged_append(const void* k, const void* v, bsa_dtype dt, int T, i
  *   o [T, Hq, d] out; lse [T, Hq] optional out.  A token that sees no key gets o = 0, lse = -inf.
  *             Rows at or after cu_q[B], and tokens beyond the max_q-th of a request, are left as
  *             they were.
- *   status    optional device int: a bounded wait that runs out writes a nonzero value there (and
- *             the rows it concerns become NaN).
+ *   status    optional device int: a bounded wait that runs out writes a nonzero value there; o
+ *             and lse are then not valid.
  *   workspace device scratch of bsa_prefix_attn_workspace_bytes() bytes, 16-byte aligned; needs no
  *             initialisation and may be reused once the stream has passed the call.  Calls that
  *             share one must not run at the same time.

@@ -9,6 +9,7 @@ library is missing, importing the binding's functions raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -702,34 +703,46 @@ PAGES_EXHAUSTED, PAGES_BAD_LENGTH, PAGES_RING, PAGES_TOKENS, PAGES_BAD_ID = 1, 2
 
 
 def _on_device(dev, *ts):
-    """Contiguous tensors of one CUDA device (None is skipped)."""
+    """Contiguous tensors of the CUDA device with index ``dev`` (None is skipped)."""
     for t in ts:
         if t is not None:
-            if t.device != dev or dev.type != "cuda":
+            if t.get_device() != dev:
                 raise ValueError("tensors must live on one CUDA device")
             if not t.is_contiguous():
                 raise ValueError("tensors must be contiguous")
 
 
+def _device_index(t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on a CUDA device")
+    return dev
+
+
+_I32 = torch.int32
+
+
 def _ints(*ts):
     for t in ts:
-        if t is not None and t.dtype != torch.int32:
+        if t is not None and t.dtype is not _I32:
             raise ValueError("index tensors must be int32")
 
 
 def _heads(x, name):
-    """Checks [T, heads, d] with contiguous heads (tokens may be strided); the token stride."""
-    if x.dim() != 3:
+    """Checks [T, heads, d] with contiguous heads (tokens may be strided); its shape and the token
+    stride."""
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [T, heads, d]")
-    if x.stride(2) != 1 or x.stride(1) != x.shape[2]:
+    if stride[2] != 1 or stride[1] != shape[2]:
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return x.stride(0)
+    return shape, stride[0]
 
 
 def _call(fn, dev, name, *args):
-    """Call a C entry on the current stream of ``dev`` (with ``dev`` current)."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    """Call a C entry on the current stream of device ``dev`` (with that device current)."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
         code = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -747,20 +760,21 @@ def page_tables(lens, new_lens, table, ring, free, page, max_tokens, pos_offset=
     ``status`` (int32 [1], optional) collects PAGES_* bits.  Returns (lens_out [B], free_out [2],
     cu_new [B + 1], slots [max_tokens], positions [max_tokens]); pass lens_out=lens and
     free_out=free to advance the state in place."""
-    dev = lens.device
+    dev = _device_index(lens)
     B = lens.numel()
-    if table.dim() != 2 or table.shape[0] != B or new_lens.numel() != B or free.numel() != 2:
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != B or new_lens.numel() != B or free.numel() != 2:
         raise ValueError("lens and new_lens must be [B], table [B, ld], free [2]")
     if lens_out is None:
         lens_out = torch.empty_like(lens)
     if free_out is None:
         free_out = torch.empty_like(free)
     if cu_new is None:
-        cu_new = torch.empty(B + 1, device=dev, dtype=torch.int32)
+        cu_new = lens.new_empty(B + 1)
     if slots is None:
-        slots = torch.empty(max_tokens, device=dev, dtype=torch.int32)
+        slots = lens.new_empty(max_tokens)
     if positions is None:
-        positions = torch.empty(max_tokens, device=dev, dtype=torch.int32)
+        positions = lens.new_empty(max_tokens)
     if (lens_out.numel() != B or free_out.numel() != 2 or cu_new.numel() != B + 1
             or slots.numel() != max_tokens or positions.numel() != max_tokens):
         raise ValueError("an output has another size")
@@ -768,7 +782,7 @@ def page_tables(lens, new_lens, table, ring, free, page, max_tokens, pos_offset=
                positions, status)
     _ints(lens, new_lens, table, ring, free, lens_out, free_out, cu_new, slots, positions, status)
     _call(lib().bsa_page_tables, dev, "bsa_page_tables", B, page, lens.data_ptr(),
-          new_lens.data_ptr(), table.data_ptr(), table.shape[1], ring.data_ptr(), ring.numel(),
+          new_lens.data_ptr(), table.data_ptr(), shape[1], ring.data_ptr(), ring.numel(),
           free.data_ptr(), lens_out.data_ptr(), free_out.data_ptr(), cu_new.data_ptr(),
           slots.data_ptr(), positions.data_ptr(), max_tokens, pos_offset,
           None if status is None else status.data_ptr())
@@ -779,31 +793,38 @@ def paged_append(k, v, slots, k_pages, v_pages):
     """Write new tokens' keys and values [T, Hk, d] to their slots [T] of the page pools
     [num_pages, Hk, page, d] (bsa_paged_append).  k and v may be slices of a fused projection:
     only the heads of a token must be contiguous.  Slots outside the pool (-1) are skipped."""
-    dev = k_pages.device
-    ks, vs = _heads(k, "k"), _heads(v, "v")
-    T, Hk, d = k.shape
-    P, page = k_pages.shape[0], k_pages.shape[2]
-    if v.shape != k.shape or slots.numel() != T:
+    shape, ks = _heads(k, "k")
+    v_shape, vs = _heads(v, "v")
+    T, Hk, d = shape
+    pool = k_pages.shape
+    if v_shape != shape or slots.numel() != T:
         raise ValueError("k and v must be [T, Hk, d], slots [T]")
-    if k_pages.shape != (P, Hk, page, d) or v_pages.shape != k_pages.shape:
+    if len(pool) != 4 or pool[1] != Hk or pool[3] != d or v_pages.shape != pool:
         raise ValueError("k_pages and v_pages must be [num_pages, Hk, page, d]")
-    if not (k.dtype == v.dtype == k_pages.dtype == v_pages.dtype):
+    dtype = k.dtype
+    if v.dtype is not dtype or k_pages.dtype is not dtype or v_pages.dtype is not dtype:
         raise ValueError("k, v and the pages must have one dtype")
+    dt = _dtype_code(k)
+    dev = _device_index(k_pages)
     _on_device(dev, slots, k_pages, v_pages)
-    if k.device != dev or v.device != dev:
+    if k.get_device() != dev or v.get_device() != dev:
         raise ValueError("tensors must live on one CUDA device")
     _ints(slots)
-    _call(lib().bsa_paged_append, dev, "bsa_paged_append", k.data_ptr(), v.data_ptr(),
-          _dtype_code(k), T, Hk, d, ks, vs, slots.data_ptr(), page, P, k_pages.data_ptr(),
-          v_pages.data_ptr())
+    _call(lib().bsa_paged_append, dev, "bsa_paged_append", k.data_ptr(), v.data_ptr(), dt, T, Hk,
+          d, ks, vs, slots.data_ptr(), pool[2], pool[0], k_pages.data_ptr(), v_pages.data_ptr())
+
+
+@functools.lru_cache(maxsize=256)
+def _prefix_attn_bytes(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q):
+    return int(lib().bsa_prefix_attn_workspace_bytes(dt, T, B, Hq, Hk, d, page, table_ld,
+                                                     prefix_len, max_q))
 
 
 def prefix_attn_workspace_bytes(dtype, T, B, Hq, Hk, d, page, table_ld, prefix_len,
                                 max_q=1) -> int:
     """Workspace bytes of prefix_attn for these sizes."""
     dt = BSA_BF16 if dtype == torch.bfloat16 else BSA_F32
-    return int(lib().bsa_prefix_attn_workspace_bytes(dt, T, B, Hq, Hk, d, page, table_ld,
-                                                     prefix_len, max_q))
+    return _prefix_attn_bytes(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q)
 
 
 def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q=None, max_q=1,
@@ -817,40 +838,42 @@ def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q
     request has; None: one token per request.  ``ws``: a uint8 device tensor of at least
     prefix_attn_workspace_bytes bytes (allocated here when None).  ``status`` (int32 [1], optional):
     set nonzero if a bounded device wait ran out.  Returns (o, lse)."""
-    dev = q.device
-    q_stride = _heads(q, "q")
-    T, Hq, d = q.shape
-    P, Hk, page = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2]
+    shape, q_stride = _heads(q, "q")
+    T, Hq, d = shape
+    pool = k_pages.shape
     B = lens.numel()
-    if k_pages.shape != (P, Hk, page, d) or v_pages.shape != k_pages.shape:
+    table_shape = table.shape
+    if len(pool) != 4 or pool[3] != d or v_pages.shape != pool:
         raise ValueError("k_pages and v_pages must be [num_pages, Hk, page, d]")
-    if table.dim() != 2 or table.shape[0] != B:
+    P, Hk, page, _ = pool
+    if len(table_shape) != 2 or table_shape[0] != B:
         raise ValueError("table must be [B, ld]")
     if cu_q is not None and cu_q.numel() != B + 1:
         raise ValueError("cu_q must be [B + 1]")
     if prefix_len > 0 and (prefix_table is None or prefix_table.numel() * page < prefix_len):
         raise ValueError("prefix_table must list ceil(prefix_len / page) pages")
-    if not (q.dtype == k_pages.dtype == v_pages.dtype):
+    dtype = q.dtype
+    if k_pages.dtype is not dtype or v_pages.dtype is not dtype:
         raise ValueError("q and the pages must have one dtype")
     dt = _dtype_code(q)
+    dev = _device_index(q)
     if o is None:
-        o = torch.empty(T, Hq, d, device=dev, dtype=q.dtype)
+        o = torch.empty_like(q)  # contiguous: q is, up to the distance of its tokens
     if lse is None:
-        lse = torch.empty(T, Hq, device=dev, dtype=torch.float32)
-    if o.shape != q.shape or o.dtype != q.dtype or lse.numel() != T * Hq \
-            or lse.dtype != torch.float32:
+        lse = q.new_empty((T, Hq), dtype=torch.float32)
+    if o.shape != shape or o.dtype is not dtype or lse.numel() != T * Hq \
+            or lse.dtype is not torch.float32:
         raise ValueError("o must be like q, lse [T, Hq] float32")
-    table_ld = table.shape[1]
-    h = lib()
+    table_ld = table_shape[1]
     if ws is None:
-        ws = torch.empty(h.bsa_prefix_attn_workspace_bytes(dt, T, B, Hq, Hk, d, page, table_ld,
-                                                           prefix_len, max_q),
-                         device=dev, dtype=torch.uint8)
+        ws = q.new_empty(_prefix_attn_bytes(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len,
+                                            max_q), dtype=torch.uint8)
     _on_device(dev, k_pages, v_pages, table, lens, prefix_table, cu_q, o, lse, ws, status)
     _ints(table, lens, prefix_table, cu_q, status)
-    _call(h.bsa_prefix_attn, dev, "bsa_prefix_attn", q.data_ptr(), q_stride, k_pages.data_ptr(),
-          v_pages.data_ptr(), dt, T, B, Hq, Hk, d, page, P, table.data_ptr(), table_ld,
-          lens.data_ptr(), None if prefix_table is None else prefix_table.data_ptr(), prefix_len,
-          None if cu_q is None else cu_q.data_ptr(), max_q, o.data_ptr(), lse.data_ptr(),
-          None if status is None else status.data_ptr(), ws.data_ptr(), ws.numel())
+    _call(lib().bsa_prefix_attn, dev, "bsa_prefix_attn", q.data_ptr(), q_stride,
+          k_pages.data_ptr(), v_pages.data_ptr(), dt, T, B, Hq, Hk, d, page, P, table.data_ptr(),
+          table_ld, lens.data_ptr(), None if prefix_table is None else prefix_table.data_ptr(),
+          prefix_len, None if cu_q is None else cu_q.data_ptr(), max_q, o.data_ptr(),
+          lse.data_ptr(), None if status is None else status.data_ptr(), ws.data_ptr(),
+          ws.numel())
     return o, lse

@@ -30,7 +30,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kPtThreads = 1024;
-constexpr int kPtMaxB = 8192;      // requests of a step (shared memory: four ints each)
+constexpr int kPtMaxB = 8192;      // requests of a step (shared memory: five ints each)
 constexpr int kPtCluster = 8;      // portable cluster size
 // Up to this many requests + new tokens one CTA does it all: above, its 1024 threads would take
 // more than a few rounds.
@@ -38,6 +38,7 @@ constexpr int kPtOneCta = 4096;
 
 struct PageTablesParams {
   int B, page_shift, ld, N, max_tokens, pos_offset;
+  bool vec4;  // slots and positions start on 16-byte boundaries
   const int *lens, *new_lens;
   int *table, *ring;
   const int* free_in;
@@ -71,11 +72,18 @@ __device__ __forceinline__ Ask ask(const PageTablesParams& p, int len, int new_l
   return a;
 }
 
+// ring index of a place `off` < N behind head
+__device__ __forceinline__ int ring_at(int head, int off, int N) {
+  const int i = head + off;  // < 2 N <= 2^28
+  return i >= N ? i - N : i;
+}
+
 __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTablesParams p) {
   extern __shared__ int sm[];
   int* s_cu = sm;                  // [B + 1] first new token of the request
   int* s_len = s_cu + p.B + 1;     // [B] tokens before; -1: not served, its tokens get no slot
-  int* s_take = s_len + p.B;       // [B] ring entries taken by the requests before it
+  int* s_new = s_len + p.B;        // [B] tokens to have
+  int* s_take = s_new + p.B;       // [B] ring entries taken by the requests before it
   int* s_drop = s_take + p.B;      // [B] pages freed by the requests before it
   __shared__ Sum3 s_warp[32];
   __shared__ long long s_taken, s_freed;
@@ -83,23 +91,26 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTable
 
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int threads = blockDim.x, warps = threads >> 5;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.B + kPtThreads - 1) / kPtThreads;  // consecutive requests of a thread
+  const int per = (p.B + threads - 1) / threads;  // consecutive requests of a thread
   if (tid == 0) {
     s_taken = 0;
     s_bits = 0;
   }
   // the ring's state, made sane: head in [0, N), avail in [0, N]
-  const int head = (int)((((long long)p.free_in[0] % p.N) + p.N) % p.N);
+  int head = p.free_in[0];
+  if (head < 0 || head >= p.N) head = (int)((((long long)head % p.N) + p.N) % p.N);
   const int avail = min(max(p.free_in[1], 0), p.N);
 
   Sum3 mine = {0, 0, 0};
   for (int k = 0; k < per; ++k) {
     const int b = tid * per + k;
     if (b >= p.B) break;
-    const int len = p.lens[b];
-    const Ask a = ask(p, len, p.new_lens[b]);
+    const int len = p.lens[b], new_len = p.new_lens[b];
+    const Ask a = ask(p, len, new_len);
     s_len[b] = len;
+    s_new[b] = new_len;
     mine = mine + Sum3{max(0, a.want - a.have), max(0, a.have - a.want), a.add};
   }
   Sum3 upto = mine;
@@ -111,7 +122,7 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTable
   if (lane == 31) s_warp[warp] = upto;
   __syncthreads();
   if (warp == 0) {
-    Sum3 w = s_warp[lane];
+    Sum3 w = lane < warps ? s_warp[lane] : Sum3{0, 0, 0};
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const Sum3 t = shfl_up3(w, o);
@@ -131,7 +142,7 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTable
     const int b = tid * per + k;
     if (b >= p.B) break;
     const int len = s_len[b];
-    const Ask a = ask(p, len, p.new_lens[b]);
+    const Ask a = ask(p, len, s_new[b]);
     const int grow = max(0, a.want - a.have);
     const bool served = !a.bad && (grow == 0 || at.grow + grow <= avail);
     if (a.bad) bits |= BSA_PAGES_BAD_LENGTH;
@@ -140,43 +151,55 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTable
     s_cu[b] = (int)min(at.add, (long long)INT_MAX);
     s_take[b] = (int)min(at.grow, (long long)INT_MAX);
     s_drop[b] = (int)min(at.drop, (long long)INT_MAX);
-    if (!served) s_len[b] = -1;
+    if (!served) {
+      s_new[b] = len;  // what it keeps
+      s_len[b] = -1;
+    }
     at = at + Sum3{grow, max(0, a.have - a.want), a.add};
   }
-  if (tid == kPtThreads - 1) {  // its exclusive sum over all requests
+  if (tid == threads - 1) {  // its exclusive sum over all requests
     s_cu[p.B] = (int)min(at.add, (long long)INT_MAX);
     if (at.add > p.max_tokens) bits |= BSA_PAGES_TOKENS;
   }
   if (taken > 0) atomicMax((unsigned long long*)&s_taken, (unsigned long long)taken);
   if (bits) atomicOr(&s_bits, bits);
-  __syncthreads();
+  if (ranks > 1) cluster.sync();  // every CTA has read lens, new_lens and free
+  else __syncthreads();
   const int freed = (int)min(s_freed, (long long)(p.N - avail));
-  if (tid == 0 && s_freed > freed) s_bits |= BSA_PAGES_RING;
-  cluster.sync();  // every CTA has read lens, new_lens and free
+  if (tid == 0 && s_freed > freed) atomicOr(&s_bits, BSA_PAGES_RING);
 
-  // pages that join and leave: a warp per request
-  for (int b = rank * 32 + warp; b < p.B; b += ranks * 32) {
-    const int new_len = p.new_lens[b];
-    const bool served = s_len[b] >= 0;
-    if (lane == 0) {
+  // pages that join and leave: a lane per request, together for one that moves many
+  for (int b0 = (rank * warps + warp) * 32; b0 < p.B; b0 += ranks * threads) {
+    const int b = b0 + lane;
+    Ask a = {0, 0, 0, true};
+    if (b < p.B) {
       p.cu_new[b] = s_cu[b];
-      if (served) p.lens_out[b] = new_len;
-      else if (p.lens_out != p.lens) p.lens_out[b] = p.lens[b];
+      p.lens_out[b] = s_new[b];
+      if (s_len[b] >= 0) a = ask(p, s_len[b], s_new[b]);
     }
-    if (!served) continue;
-    const Ask a = ask(p, s_len[b], new_len);
-    int* row = p.table + (size_t)b * p.ld;
-    for (int i = lane; i < a.want - a.have; i += 32)
-      row[a.have + i] = p.ring[(int)(((long long)head + s_take[b] + i) % p.N)];
-    for (int i = lane; i < a.have - a.want; i += 32) {
-      const long long at_i = (long long)s_drop[b] + i;
-      if (at_i < freed) p.ring[(int)((head + avail + at_i) % p.N)] = row[a.want + i];
+    const int moves = abs(a.want - a.have);
+    auto move = [&](int req, int have, int want, int i) {
+      int* row = p.table + (size_t)req * p.ld;
+      if (want > have) {
+        row[have + i] = p.ring[ring_at(head, s_take[req] + i, p.N)];
+      } else {
+        const long long off = (long long)s_drop[req] + i;
+        if (off < freed) p.ring[ring_at(head, avail + (int)off, p.N)] = row[want + i];
+      }
+    };
+    if (moves == 1) move(b, a.have, a.want, 0);
+    for (uint32_t many = __ballot_sync(0xffffffffu, moves > 1); many; many &= many - 1) {
+      const int src = __ffs(many) - 1;
+      const int have = __shfl_sync(0xffffffffu, a.have, src);
+      const int want = __shfl_sync(0xffffffffu, a.want, src);
+      for (int i = lane; i < abs(want - have); i += 32) move(b0 + src, have, want, i);
     }
   }
 
-  // slots and positions of the new tokens
+  // slots and positions of the new tokens, four a thread
   const int total = s_cu[p.B];
-  for (int t0 = (rank * kPtThreads + tid) * 4; t0 < p.max_tokens; t0 += ranks * kPtThreads * 4) {
+  const int page_mask = (1 << p.page_shift) - 1;
+  for (int t0 = (rank * threads + tid) * 4; t0 < p.max_tokens; t0 += ranks * threads * 4) {
     int lo = 0;  // the last request whose range starts at or before t0
     if (t0 < total) {
       int hi = p.B;
@@ -198,31 +221,37 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTable
       const int own = len + (t - s_cu[lo]);
       const int c = own >> p.page_shift;
       if (c != page_at || lo != page_b) {
-        const int have = (len + (1 << p.page_shift) - 1) >> p.page_shift;
+        const int have = (int)(((long long)len + page_mask) >> p.page_shift);
         id = c < have ? p.table[(size_t)lo * p.ld + c]
-                      : p.ring[(int)(((long long)head + s_take[lo] + (c - have)) % p.N)];
+                      : p.ring[ring_at(head, s_take[lo] + (c - have), p.N)];
         page_at = c;
         page_b = lo;
         if (id < 0 || id >= p.N) {
           id = -1;
-          atomicOr(&s_bits, BSA_PAGES_BAD_ID);
+          if (t < p.max_tokens) atomicOr(&s_bits, BSA_PAGES_BAD_ID);
         }
       }
-      if (id >= 0) slot[e] = (id << p.page_shift) + (own & ((1 << p.page_shift) - 1));
+      if (id >= 0) slot[e] = (id << p.page_shift) + (own & page_mask);
       pos[e] = own + p.pos_offset;
     }
+    if (p.vec4 && t0 + 4 <= p.max_tokens) {
+      *reinterpret_cast<int4*>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      if (p.positions)
+        *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (t0 + e >= p.max_tokens) break;
-      p.slots[t0 + e] = slot[e];
-      if (p.positions) p.positions[t0 + e] = pos[e];
+      for (int e = 0; e < 4; ++e) {
+        if (t0 + e >= p.max_tokens) break;
+        p.slots[t0 + e] = slot[e];
+        if (p.positions) p.positions[t0 + e] = pos[e];
+      }
     }
   }
   __syncthreads();
   if (tid == 0) {
     if (rank == 0) {
       p.cu_new[p.B] = total;
-      p.free_out[0] = (int)((head + s_taken) % p.N);
+      p.free_out[0] = ring_at(head, (int)s_taken, p.N);
       p.free_out[1] = (int)(avail - s_taken + freed);
     }
     if (s_bits && p.status) atomicOr(p.status, s_bits);
@@ -297,10 +326,11 @@ extern "C" bsa_status bsa_page_tables(int B, int page, const int* lens, const in
   BSA_REQUIRE(pos_offset >= 0 && (long long)pos_offset + ((long long)table_ld << shift) <= INT_MAX,
               BSA_ERR_ARG);
   BSA_REQUIRE(max_tokens <= INT_MAX - kPtCluster * kPtThreads * 4, BSA_ERR_UNSUPPORTED);
-  PageTablesParams p = {B,    shift, table_ld, num_pages, max_tokens, pos_offset, lens, new_lens,
-                        table, ring, free_in,  lens_out,  free_out,   cu_new,     slots, positions,
-                        status};
-  const int smem = (4 * B + 1) * (int)sizeof(int);
+  PageTablesParams p = {B,        shift,    table_ld, num_pages, max_tokens, pos_offset,
+                        all_aligned16(slots, positions),
+                        lens,     new_lens, table,    ring,      free_in,    lens_out,
+                        free_out, cu_new,   slots,    positions, status};
+  const int smem = (5 * B + 1) * (int)sizeof(int);
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
           cudaSuccess) {
@@ -309,12 +339,14 @@ extern "C" bsa_status bsa_page_tables(int B, int page, const int* lens, const in
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  const unsigned ctas = (long long)B + max_tokens <= kPtOneCta ? 1u : (unsigned)kPtCluster;
+  const long long work = (long long)B + max_tokens;
+  const unsigned ctas = work <= kPtOneCta ? 1u : (unsigned)kPtCluster;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kPtThreads);
+  // a small step needs no more threads than it has items; fewer warps meet faster at the barriers
+  cfg.blockDim = dim3(work <= 256 ? 256 : kPtThreads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;

@@ -47,6 +47,8 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
   extern __shared__ __align__(16) float smf[];
   float *sq = smf + L::kQ, *sk = smf + L::kK, *sv = smf + L::kV, *sp = smf + L::kP;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  pdl_wait();
+  pdl_trigger();
 
   // the unit: rows r0 .. r0 + nrows of kv head h (row = token * G + head of the group), keys
   // [0, n) on `pages`; row r sees keys j <= first_pos + r / G
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
     pages = p.table + (size_t)b * p.table_ld;
     // tiles start at whole tokens: G divides RG
     first_pos = r.len - r.nq + tile * (RG / p.G);
-    n = max(0, min(r.len, first_pos + (nrows - 1) / p.G + 1));
+    n = max(0, min(r.len, first_pos + ((nrows - 1) >> p.g_shift) + 1));
     slot = p.ns1 + piece;
     pieces = p.ns2;
   }
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
   const long long rows = (long long)p.T * p.Hq;
   auto row_id = [&](int r) {  // of the partial results: token * Hq + query head
     const int rr = r0 + r;
-    return (long long)(rr / p.G) * p.Hq + h * p.G + rr % p.G;
+    return (long long)((rr >> p.g_shift)) * p.Hq + h * p.G + (rr & (p.G - 1));
   };
   float m[TM], l[TM], acc[TM][DC * 4];
 #pragma unroll
@@ -106,8 +108,8 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
       float x[4] = {0.f, 0.f, 0.f, 0.f};
       if (r < nrows) {
         const int rr = r0 + r;
-        load_vec<T, 4>(static_cast<const T*>(p.q) + (rr / p.G) * p.q_stride +
-                           (long long)(h * p.G + rr % p.G) * D + c, x);
+        load_vec<T, 4>(static_cast<const T*>(p.q) + ((rr >> p.g_shift)) * p.q_stride +
+                           (long long)(h * p.G + (rr & (p.G - 1))) * D + c, x);
       }
       *reinterpret_cast<float4*>(sq + r * L::kLd + c) =
           make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale);
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
     }
 #pragma unroll
     for (int a = 0; a < TM; ++a) {
-      const int last = first_pos + (ty * TM + a) / p.G;
+      const int last = first_pos + ((ty * TM + a) >> p.g_shift);
       float top = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -234,6 +236,7 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
 template <typename T, int D>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p) {
   constexpr int C = D / 32;
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const long long rows = (long long)p.T * p.Hq;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p)
   // the row's pieces: dense ones, then up to two runs of item slots
   int first[2] = {0, 0}, count[2] = {0, 0}, at[2] = {0, 0};
   if (p.item_ctas) {
-    const int h = hq / p.G, g = hq - h * p.G;
+    const int h = hq >> p.g_shift, g = hq - h * p.G;
     auto pieces = [&](int k, int item, int r) {
       const int2 c = p.item_cta[item];  // cut: a run that stopped early has not written it
       const int c0 = min(max(c.x, 0), p.item_ctas - 1), c1 = min(max(c.y, c0), p.item_ctas - 1);
@@ -280,24 +283,17 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p)
       o = p.item_o + i * D;
     }
   };
-  float top = -INFINITY;
-  for (int s = lane; s < n; s += 32) {
-    const float2* ml;
-    const float* o;
-    piece(s, ml, o);
-    top = fmaxf(top, ml->x);
-  }
-  top = warp_max(top);
-  float acc[C], l = 0.f;
+  // running maximum and sum over the pieces, kAhead of them loaded together
+  constexpr int kAhead = 8;
+  float top = -INFINITY, l = 0.f, acc[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) acc[c] = 0.f;
-  constexpr int kAhead = 4;  // pieces loaded together
   for (int s0 = 0; s0 < n; s0 += kAhead) {
     float2 ml[kAhead];
     float x[kAhead][C];
 #pragma unroll
     for (int e = 0; e < kAhead; ++e) {
-      ml[e] = make_float2(0.f, 0.f);
+      ml[e] = make_float2(-INFINITY, 0.f);
       if (s0 + e < n) {
         const float2* mp;
         const float* op;
@@ -306,6 +302,14 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p)
         load_vec<float, C>(op + lane * C, x[e]);
       }
     }
+    float m = top;
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) m = fmaxf(m, ml[e].x);
+    const float keep = m == -INFINITY ? 1.f : exp2f(top - m);
+    top = m;
+    l *= keep;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] *= keep;
 #pragma unroll
     for (int e = 0; e < kAhead; ++e) {
       if (ml[e].y == 0.f) continue;  // no key in the piece: its o was not written
@@ -404,15 +408,12 @@ bsa_status launch_simt(const PrefixParams& p, const PrefixPlan& w, cudaStream_t 
   const long long units2 = (long long)p.B * w.simt2 * p.Hk * p.ns2;
   if (units1 + units2 > INT_MAX) return BSA_ERR_UNSUPPORTED;
   if (units1 + units2 == 0) return BSA_OK;
-  auto kern = prefix_simt_kernel<T, D, RG>;
   const int smem = SimtSmem<D, RG>::kTotal;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess) {
-    (void)cudaGetLastError();
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_smem(prefix_simt_kernel<T, D, RG>, smem, done) ||
+      !launch_pdl(prefix_simt_kernel<T, D, RG>, (int)(units1 + units2), kPsThreads, smem, st, p,
+                  SimtGrid{(int)units1, w.simt2}))
     return BSA_ERR_CUDA;
-  }
-  kern<<<(int)(units1 + units2), kPsThreads, smem, st>>>(p, SimtGrid{(int)units1, w.simt2});
-  BSA_LAUNCH_CHECK();
   return BSA_OK;
 }
 
@@ -422,7 +423,7 @@ bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status,
     const bsa_status rc = prefix_attn_tc(p, D, w.tc1, w.tc2, w.fused, w.direct, status, st);
     if (rc != BSA_OK || w.direct) return rc;
     if (w.rows) {
-      const bsa_status rr = prefix_attn_rows(p, D, w.rows_prefix, status, st);
+      const bsa_status rr = prefix_attn_rows(p, D, w.rows_prefix, w.tc1 > 0, status, st);
       if (rr != BSA_OK) return rr;
     }
   }
@@ -432,9 +433,9 @@ bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status,
     if (rc != BSA_OK) return rc;
   }
   const long long rows = (long long)p.T * p.Hq;
-  prefix_merge_kernel<T, D><<<(int)((rows + 7) / 8), 256, 0, st>>>(p);
-  BSA_LAUNCH_CHECK();
-  return BSA_OK;
+  return launch_pdl(prefix_merge_kernel<T, D>, (int)((rows + 7) / 8), 256, 0, st, p)
+             ? BSA_OK
+             : BSA_ERR_CUDA;
 }
 
 bool sizes_ok(int T, int B, int Hq, int Hk, int d, int page, int table_ld, int prefix_len,
@@ -493,6 +494,7 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
   p.q = q; p.k = k_pages; p.v = v_pages;
   p.q_stride = T <= 1 ? (long long)Hq * d : q_stride;
   p.T = T; p.B = B; p.Hq = Hq; p.Hk = Hk; p.G = Hq / Hk;
+  p.g_shift = p.G == 1 ? 0 : p.G == 2 ? 1 : p.G == 4 ? 2 : 3;
   p.page_shift = page_shift_of(page);
   p.num_pages = num_pages;
   p.table = table; p.table_ld = table_ld; p.lens = lens;

@@ -14,14 +14,13 @@
 //              the row maxima meet in shared memory, each warp exponentiates its keys, P meets in
 //              shared memory, then each warp multiplies all 64 keys into its d / 4 output columns,
 //              so no accumulator is joined across warps
-//   warp 4:    TMA producer; lane i loads box i (a page, or 64 rows of one) of K and V
+//   warp 4:    TMA producer; lane i loads box i (a page, or 64 rows of one) of K and V, and with a
+//              piece's first tile its query rows.  Its lanes hold the ranges of the next 32
+//              requests, and page ids are read a tile ahead, so that an item border costs it no
+//              wait for memory (items of one tile took 5 us each before, 64 x 64 tokens x 8 heads
+//              15.8 us in all)
 // V rows without a key are masked to zero in the registers that feed the products.
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "prefix_attn.cuh"
-#include "tc_common.cuh"
 
 namespace bsa {
 namespace {
@@ -36,19 +35,23 @@ struct RowsSmem {
   static constexpr int kTile = (D / 64) * kHalf;     // K or V
   static constexpr int kStages = D == 128 ? 3 : 6;   // 96 KB in flight per CTA
   static constexpr int kP = kStages * 2 * kTile;     // two buffers of [16 x 64] bf16
-  static constexpr int kTotal = kP + 2 * 2048;
+  static constexpr int kQTile = (D / 64) * 2048;     // 16 query rows: [D / 64][16 x 128 B]
+  static constexpr int kQ = kP + 2 * 2048;           // two buffers: of alternate pieces
+  static constexpr int kTotal = kQ + 2 * kQTile;
 };
 
 // What the producer tells the consumers about a tile.
 struct TileInfo {
-  int item, h, t0, nrows, first_pos;
+  int item, nrows, first_pos;
   int j0, n;      // its first key; keys of the item
   uint32_t have;  // boxes on pages of the pool | first tile of the run's piece << 8 | last << 9
+                  // | query buffer << 10
 };
 
 struct RowsGrid {
   int prefix_items;  // Hk, or 0: the prefix is not this kernel's part
   int box_shift;     // rows of a box
+  int after_tc;      // a kernel of the same call runs before: its results are not read here
   int* status;
 };
 
@@ -80,19 +83,24 @@ __device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, 128;
 
 template <int D>
 __global__ void __launch_bounds__(kRThreads, 2)
-    prefix_rows_kernel(const __grid_constant__ CUtensorMap tmk,
+    prefix_rows_kernel(const __grid_constant__ CUtensorMap tmq,
+                       const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const PrefixParams p,
                        const RowsGrid g) {
   using L = RowsSmem<D>;
   constexpr int NT = D / 32;  // 8-column output tiles of a warp
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_align1024(smem_raw);
-  __shared__ __align__(8) uint64_t full[L::kStages], empty[L::kStages];
+  __shared__ __align__(8) uint64_t full[L::kStages], empty[L::kStages], q_free[2];
   __shared__ TileInfo s_info[L::kStages];
   __shared__ long long s_sum[kRThreads];
   __shared__ float s_max[2][4][16], s_l[2][4][16];
   __shared__ int s_abort, s_stop;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // Behind the tensor-core kernel the inputs are already there (it has waited for them before it
+  // let this one start); its own results are only the merge's concern, which waits for this kernel.
+  if (!g.after_tc) pdl_wait();
+  pdl_trigger();
 
   // tiles of all requests, a run of consecutive requests per thread
   const int per = (p.B + kRThreads - 1) / kRThreads;
@@ -105,6 +113,8 @@ __global__ void __launch_bounds__(kRThreads, 2)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 4);
     }
+    mbar_init(&q_free[0], 4);
+    mbar_init(&q_free[1], 4);
     fence_mbar_init();
     s_abort = s_stop = 0;
   }
@@ -128,101 +138,132 @@ __global__ void __launch_bounds__(kRThreads, 2)
   const long long total = (long long)p.Hk * (ptiles + s_sum[kRThreads - 1]);
   // no CTA within a run of pieces may be without one: at most as many CTAs work as there are tiles
   const long long ctas = min((long long)gridDim.x, total);
-  if (blockIdx.x >= ctas) return;
+  if (blockIdx.x >= ctas) {
+    if (g.after_tc) pdl_wait();  // this kernel is not complete before the one before it
+    return;
+  }
   const long long f0 = total * blockIdx.x / ctas, f1 = total * (blockIdx.x + 1) / ctas;
   const int count = (int)(f1 - f0);
 
   if (warp == 4) {
     // ------------------------------------------------------------------------- producer
-    // the item and the tile of it that the run starts with
-    int b = -1, h, tile, tiles;  // b = -1: the prefix
-    PaRequest r = {};
-    auto enter = [&](int nb) {
-      b = nb;
-      r = pa_request(p, b);
-      tiles = (pa_own_keys(p, r) + kRKeys - 1) / kRKeys;
+    // where the run is: request (-1: the prefix), kv head, tile of the item
+    struct Place {
+      int b, h, tile, tiles, n, t0, nrows, first_pos;
+    } c;
+    // the ranges of requests base .. base + 31, one per lane
+    int base = -64;
+    PaRequest mine_r = {};
+    auto enter = [&](Place& x, int b) {
+      if (b >= base + 32) {
+        base = b;
+        mine_r = pa_request(p, min(b + lane, p.B - 1));
+      }
+      PaRequest r;
+      r.t0 = __shfl_sync(0xffffffffu, mine_r.t0, b - base);
+      r.nq = __shfl_sync(0xffffffffu, mine_r.nq, b - base);
+      r.len = __shfl_sync(0xffffffffu, mine_r.len, b - base);
+      x.b = b;
+      x.n = pa_own_keys(p, r);
+      x.tiles = (x.n + kRKeys - 1) / kRKeys;
+      x.t0 = r.t0;
+      x.nrows = min(r.nq, p.max_q) << p.g_shift;
+      x.first_pos = r.len - r.nq;
     };
     if (f0 < (long long)p.Hk * ptiles) {
-      h = (int)(f0 / ptiles);
-      tile = (int)(f0 - (long long)h * ptiles);
-      tiles = ptiles;
+      c.b = -1;
+      c.h = (int)(f0 / ptiles);
+      c.tile = (int)(f0 - (long long)c.h * ptiles);
+      c.tiles = ptiles;
+      c.n = c.first_pos = p.prefix_len;
+      c.t0 = 0;
+      c.nrows = pa_tokens(p) << p.g_shift;
     } else {
       const long long f = f0 - (long long)p.Hk * ptiles;
       int th = 0;
       while ((long long)p.Hk * s_sum[th] <= f) ++th;
       long long before = th ? s_sum[th - 1] : 0;
-      enter(th * per);
-      while ((long long)p.Hk * (before + tiles) <= f) {
-        before += tiles;
-        enter(b + 1);
+      enter(c, th * per);
+      while ((long long)p.Hk * (before + c.tiles) <= f) {
+        before += c.tiles;
+        enter(c, c.b + 1);
       }
       const int rest = (int)(f - (long long)p.Hk * before);
-      h = rest / tiles;
-      tile = rest - h * tiles;
+      c.h = rest / c.tiles;
+      c.tile = rest - c.h * c.tiles;
     }
     const int boxes = kRKeys >> g.box_shift;
     const uint32_t box_bytes = (uint32_t)(128 << g.box_shift);
     const uint64_t pol = l2_evict_first();
-    bool ok = true;
-    bool first = true;
-    int done = 0;
+    // the page of the lane's box at a place, -1: nothing to load
+    auto page_at = [&](const Place& x) {
+      const int j = x.tile * kRKeys + (lane << g.box_shift);
+      if (lane >= boxes || j >= x.n) return -1;
+      const int id = (x.b < 0 ? p.ptable : p.table + (size_t)x.b * p.table_ld)[j >> p.page_shift];
+      return id < p.num_pages ? id : -1;
+    };
+    bool ok = true, first = true;
+    int done = 0, piece = 0;
+    int id = page_at(c);
     for (; done < count; ++done) {
       const int st = done % L::kStages;
-      const int n = b < 0 ? p.prefix_len : pa_own_keys(p, r);
-      const int j = tile * kRKeys + (lane << g.box_shift);
-      int id = -1;
-      if (lane < boxes && j < n) {
-        const int* pages = b < 0 ? p.ptable : p.table + (size_t)b * p.table_ld;
-        id = pages[j >> p.page_shift];
-        if (id >= p.num_pages) id = -1;
+      const bool ends = c.tile + 1 == c.tiles;
+      // the next place, and its pages on their way
+      Place nx = c;
+      if (!ends) {
+        ++nx.tile;
+      } else if (done + 1 < count) {
+        nx.tile = 0;
+        if (++nx.h == p.Hk) {
+          nx.h = 0;
+          do {
+            ok = nx.b + 1 < p.B;  // holds unless the lengths change under the call
+            if (ok) enter(nx, nx.b + 1);
+          } while (ok && nx.tiles == 0);
+          if (!ok) break;
+        }
       }
+      const int next_id = done + 1 < count ? page_at(nx) : -1;
       const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
-      const bool last = tile + 1 == tiles || done + 1 == count;
+      const bool last = ends || done + 1 == count;
       if (done >= L::kStages) ok = mbar_wait_bounded(&empty[st], ((done / L::kStages) - 1) & 1);
+      if (first && piece >= 2)
+        ok = ok && mbar_wait_bounded(&q_free[piece & 1], ((piece >> 1) - 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const int item = b < 0 ? h : g.prefix_items + b * p.Hk + h;
       if (lane == 0) {
         TileInfo t;
-        t.item = item;
-        t.h = h;
-        t.t0 = b < 0 ? 0 : r.t0;
-        t.nrows = b < 0 ? pa_tokens(p) * p.G : min(r.nq, p.max_q) * p.G;
-        t.first_pos = b < 0 ? n : r.len - r.nq;
-        t.j0 = tile * kRKeys;
-        t.n = n;
-        t.have = have | (first ? 256u : 0u) | (last ? 512u : 0u);
+        t.item = c.b < 0 ? c.h : g.prefix_items + c.b * p.Hk + c.h;
+        t.nrows = c.nrows;
+        t.first_pos = c.first_pos;
+        t.j0 = c.tile * kRKeys;
+        t.n = c.n;
+        t.have = have | (first ? 256u : 0u) | (last ? 512u : 0u) | (uint32_t)(piece & 1) << 10;
         s_info[st] = t;
-        if (tile == 0) p.item_cta[item].x = blockIdx.x;
-        if (tile + 1 == tiles) p.item_cta[item].y = blockIdx.x;
-        mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(have) * box_bytes * (D / 64) * 2);
+        if (c.tile == 0) p.item_cta[t.item].x = blockIdx.x;
+        if (ends) p.item_cta[t.item].y = blockIdx.x;
+        mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(have) * box_bytes * (D / 64) * 2 +
+                                             (first ? (uint32_t)L::kQTile : 0u));
+        if (first)
+          for (int hf = 0; hf < D / 64; ++hf)
+            tma_load_q(smem + L::kQ + (piece & 1) * L::kQTile + hf * 2048, &tmq, hf * 64, c.h, c.t0,
+                       &full[st]);
       }
       __syncwarp();
       if (id >= 0) {
         // a page of 128 holds two boxes
-        const int y = ((id * p.Hk + h) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
+        const int j = c.tile * kRKeys + (lane << g.box_shift);
+        const int y = ((id * p.Hk + c.h) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
         unsigned char* dst = smem + st * 2 * L::kTile + lane * box_bytes;
         for (int hf = 0; hf < D / 64; ++hf)
           tc::tma_load_2d_hint(dst + hf * L::kHalf, &tmk, hf * 64, y, &full[st], pol);
         for (int hf = 0; hf < D / 64; ++hf)
           tc::tma_load_2d_hint(dst + L::kTile + hf * L::kHalf, &tmv, hf * 64, y, &full[st], pol);
       }
+      if (last) ++piece;
       first = last;
-      // the next tile; done + 1 < count says that there is one
-      if (++tile == tiles && done + 1 < count) {
-        tile = 0;
-        if (++h == p.Hk) {
-          h = 0;
-          do {
-            ok = b + 1 < p.B;  // holds unless the lengths change under the call
-            if (ok) enter(b + 1);
-          } while (ok && tiles == 0);
-          if (!ok) {
-            ++done;
-            break;
-          }
-        }
-      }
+      c = nx;
+      id = next_id;
     }
     if (!ok && lane == 0) s_abort = 1;
     // copies still in flight land before the CTA leaves, whatever the consumers do
@@ -247,17 +288,14 @@ __global__ void __launch_bounds__(kRThreads, 2)
       }
       const TileInfo t = s_info[st];
       if (t.have & 256u) {  // a new piece
+        const int qb = (t.have >> 10) & 1;
+        const uint32_t qt = smem_u32(smem + L::kQ + qb * L::kQTile);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int row = qr + (e & 1) * 8;
-            q[kk][e] = 0u;
-            if (row < t.nrows)
-              q[kk][e] = *reinterpret_cast<const uint32_t*>(
-                  static_cast<const __nv_bfloat16*>(p.q) + (t.t0 + row / p.G) * p.q_stride +
-                  (t.h * p.G + row % p.G) * D + kk * 16 + (e >> 1) * 8 + qc);
-          }
+          ldsm4(q[kk], qt + (kk >> 2) * 2048 +
+                           tc::sw128_offset(mrow + (mat & 1) * 8, (kk & 3) * 2 + (mat >> 1)));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_free[qb]);
 #pragma unroll
         for (int c = 0; c < NT; ++c)
 #pragma unroll
@@ -281,7 +319,8 @@ __global__ void __launch_bounds__(kRThreads, 2)
       const bool part = left < kRKeys || (t.have & all) != all;
       // a key of the tile that exists
       auto is_key = [&](int j) { return j < left && ((t.have >> (j >> g.box_shift)) & 1); };
-      const int pos[2] = {t.first_pos + qr / p.G - t.j0, t.first_pos + (qr + 8) / p.G - t.j0};
+      const int pos[2] = {t.first_pos + (qr >> p.g_shift) - t.j0,
+                          t.first_pos + ((qr + 8) >> p.g_shift) - t.j0};
       if (part || pos[0] < kRKeys - 1) {  // rows only look further down the tile
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -387,59 +426,32 @@ __global__ void __launch_bounds__(kRThreads, 2)
   }
   __syncthreads();
   if (s_abort && tid == 0) report_timeout(g.status, 6);
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    else
-      (void)cudaGetLastError();
-  });
-  return fn;
+  if (g.after_tc) pdl_wait();  // this kernel is not complete before the one before it
 }
 
 template <int D>
 bsa_status launch_rows(const PrefixParams& p, const RowsGrid& g, cudaStream_t st) {
-  auto enc = encode_fn();
-  if (!enc) return BSA_ERR_CUDA;
-  CUtensorMap tm[2];
-  for (int kv = 0; kv < 2; ++kv) {
-    const cuuint32_t ones[2] = {1, 1};
-    cuuint64_t dims[2] = {(cuuint64_t)D, ((cuuint64_t)p.num_pages * p.Hk) << p.page_shift};
-    cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)1 << g.box_shift};
-    if (enc(&tm[kv], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(kv ? p.v : p.k), dims,
-            strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return BSA_ERR_CUDA;
-  }
-  const int smem = RowsSmem<D>::kTotal + 1024;  // + alignment slack
-  auto kern = prefix_rows_kernel<D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess) {
-    (void)cudaGetLastError();
+  CUtensorMap tmq, tmk, tmv;
+  if (!prefix_q_map(&tmq, p, D, 16) || !prefix_kv_map(&tmk, p.k, p, D, g.box_shift) ||
+      !prefix_kv_map(&tmv, p.v, p, D, g.box_shift))
     return BSA_ERR_CUDA;
-  }
-  kern<<<p.item_ctas, kRThreads, smem, st>>>(tm[0], tm[1], p, g);
-  BSA_LAUNCH_CHECK();
+  const int smem = RowsSmem<D>::kTotal + 1024;  // + alignment slack
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_smem(prefix_rows_kernel<D>, smem, done) ||
+      !launch_pdl(prefix_rows_kernel<D>, p.item_ctas, kRThreads, smem, st, tmq, tmk, tmv, p, g))
+    return BSA_ERR_CUDA;
   return BSA_OK;
 }
 
 }  // namespace
 
 // Own keys of every request and, with `prefix`, the prefix, for up to 16 rows each.
-bsa_status prefix_attn_rows(const PrefixParams& p, int d, bool prefix, int* status,
+bsa_status prefix_attn_rows(const PrefixParams& p, int d, bool prefix, bool after_tc, int* status,
                             cudaStream_t st) {
   RowsGrid g;
   g.prefix_items = prefix ? p.Hk : 0;
   g.box_shift = std::min(p.page_shift, 6);
+  g.after_tc = after_tc;
   g.status = status;
   return d == 64 ? launch_rows<64>(p, g, st) : launch_rows<128>(p, g, st);
 }

@@ -29,7 +29,6 @@
 #include <mutex>
 
 #include "prefix_attn.cuh"
-#include "tc_common.cuh"
 
 namespace bsa {
 namespace {
@@ -80,14 +79,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z,
-                                            int w, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-      : "memory");
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -114,7 +105,7 @@ __device__ __forceinline__ Unit unit_of(const PrefixParams& p, const TcGrid& g) 
     const int tile = i % g.tiles1;
     u.h = i / g.tiles1;
     u.r0 = tile * 256;
-    u.t0 = u.r0 / p.G;
+    u.t0 = u.r0 >> p.g_shift;
     u.nrows = min(256, pa_tokens(p) * p.G - u.r0);
     u.n0 = p.prefix_len;
     u.n1 = 0;
@@ -132,12 +123,12 @@ __device__ __forceinline__ Unit unit_of(const PrefixParams& p, const TcGrid& g) 
     const int b = i % p.B;
     u.h = i / p.B;
     const PaRequest r = pa_request(p, b);
-    u.t0 = r.t0 + tile * (256 / p.G);
+    u.t0 = r.t0 + tile * (256 >> p.g_shift);
     u.r0 = u.t0 * p.G;
     u.nrows = min(256, min(r.nq, p.max_q) * p.G - tile * 256);
-    u.first_pos = r.len - r.nq + tile * (256 / p.G);
+    u.first_pos = r.len - r.nq + tile * (256 >> p.g_shift);
     u.n0 = g.fused ? p.prefix_len : 0;
-    u.n1 = max(0, min(r.len, u.first_pos + (u.nrows - 1) / p.G + 1));
+    u.n1 = max(0, min(r.len, u.first_pos + ((u.nrows - 1) >> p.g_shift) + 1));
     u.own = p.table + (size_t)b * p.table_ld;
     u.slot = p.ns1 + piece;
     pieces = p.ns2;
@@ -173,12 +164,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
   __shared__ uint32_t s_mask[kXMasks];  // boxes of the key tile that are on pages of the pool
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
   const Unit u = unit_of(p, g);
   if (u.nrows <= 0) return;
   const long long rows = (long long)p.T * p.Hq;
   auto row_id = [&](int r) {
     const int rr = u.r0 + r;
-    return (long long)(rr / p.G) * p.Hq + u.h * p.G + rr % p.G;
+    return (long long)(rr >> p.g_shift) * p.Hq + u.h * p.G + (rr & (p.G - 1));
   };
   if (u.tile0 >= u.tile1) {  // no key: rows of sum 0
     for (int r = tid; r < u.nrows; r += kXThreads) {
@@ -239,8 +232,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
       mbar_arrive_expect_tx(q_full, (wide ? 2 : 1) * L::kTile);
       for (int s = 0; s < (wide ? 2 : 1); ++s)
         for (int hf = 0; hf < kHalves; ++hf)
-          tma_load_4d(smem + L::kQ + s * L::kTile + hf * 16384, &tmq, hf * 64, 0, u.h,
-                      u.t0 + s * (128 / p.G), q_full);
+          tma_load_q(smem + L::kQ + s * L::kTile + hf * 16384, &tmq, hf * 64, u.h,
+                     u.t0 + s * (128 >> p.g_shift), q_full);
     }
     // the page of lane's box in tile t, -1: nothing to load
     auto page_of = [&](int t) -> int {
@@ -371,7 +364,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int row = r + (wide ? 128 * s : 0);             // row of the unit
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float scale = rsqrtf((float)D) * kPaLog2e;
-    const int pos = u.first_pos + row / p.G;
+    const int pos = u.first_pos + (row >> p.g_shift);
     const int ns = steps(s);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -565,42 +558,43 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 template <int D>
 bsa_status launch_tc(const PrefixParams& p, const TcGrid& g, int grid, cudaStream_t st) {
   CUtensorMap tmq, tmk, tmv;
-  auto enc = encode_fn();
-  if (!enc) return BSA_ERR_CUDA;
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
-  {
-    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)p.G, (cuuint64_t)p.Hk, (cuuint64_t)p.T};
-    cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)p.G * D * 2,
-                             (cuuint64_t)p.q_stride * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)p.G, 1, (cuuint32_t)(128 / p.G)};
-    if (enc(&tmq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.q), dims, strides, box,
-            ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return BSA_ERR_CUDA;
-  }
-  for (int kv = 0; kv < 2; ++kv) {
-    cuuint64_t dims[2] = {(cuuint64_t)D, ((cuuint64_t)p.num_pages * p.Hk) << p.page_shift};
-    cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-    cuuint32_t box[2] = {64, (cuuint32_t)1 << g.box_shift};
-    if (enc(kv ? &tmv : &tmk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-            const_cast<void*>(kv ? p.v : p.k), dims, strides, box, ones,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return BSA_ERR_CUDA;
-  }
-  const int smem = TcSmem<D>::kTotal + 1024;  // + alignment slack
-  auto kern = prefix_tc_kernel<D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess) {
-    (void)cudaGetLastError();
+  if (!prefix_q_map(&tmq, p, D, 128) || !prefix_kv_map(&tmk, p.k, p, D, g.box_shift) ||
+      !prefix_kv_map(&tmv, p.v, p, D, g.box_shift))
     return BSA_ERR_CUDA;
-  }
-  kern<<<grid, kXThreads, smem, st>>>(tmq, tmk, tmv, p, g);
-  BSA_LAUNCH_CHECK();
+  const int smem = TcSmem<D>::kTotal + 1024;  // + alignment slack
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_smem(prefix_tc_kernel<D>, smem, done) ||
+      !launch_pdl(prefix_tc_kernel<D>, grid, kXThreads, smem, st, tmq, tmk, tmv, p, g))
+    return BSA_ERR_CUDA;
   return BSA_OK;
 }
 
 }  // namespace
+
+bool prefix_q_map(CUtensorMap* m, const PrefixParams& p, int d, int rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)p.G, (cuuint64_t)p.Hk, (cuuint64_t)p.T};
+  const cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)p.G * d * 2,
+                                 (cuuint64_t)p.q_stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)p.G, 1, (cuuint32_t)(rows >> p.g_shift)};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.q), dims, strides, box,
+             ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool prefix_kv_map(CUtensorMap* m, const void* pool, const PrefixParams& p, int d, int box_shift) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint32_t ones[2] = {1, 1};
+  const cuuint64_t dims[2] = {(cuuint64_t)d, ((cuuint64_t)p.num_pages * p.Hk) << p.page_shift};
+  const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)1 << box_shift};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dims, strides, box,
+             ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // The units of a plan on the tensor cores: packed rows x prefix (tiles1 > 0, p.ns1 pieces) and
 // requests x own keys (tiles2 > 0, p.ns2 pieces; `fused`: prefix and own keys).

@@ -61,14 +61,50 @@ struct TcGrid {
   int* status;
 };
 
-// D[tmem] (+)= A[tmem] x B[smem desc]
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
+// Issue by a warp in step: `leader` is nonzero in the one lane that issues.  The operands are the
+// same in all lanes and the warp does not branch, so they stay in uniform registers, which the
+// instruction reads; built inside a one-lane branch they are moved there one by one, and 16
+// products a step then cost the issuing warp more than the tensor cores (2.6 us a step and unit of
+// 256 x 128 scores instead of 1.4).  A descriptor is a constant high word and a low word, start
+// address / 16 and the leading offset.
+__device__ __forceinline__ int elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
+  return (int)r;
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // rows of 8 x 128 B, swizzled
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr, uint32_t lbo_bytes) {
+  return (smem_addr >> 4) | ((lbo_bytes >> 4) << 16);
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(int leader, uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                       uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred e, c;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.s32 e, %0, 0;\n\tsetp.ne.b32 c, %6, 0;\n\t"
+      "mov.b64 a, {%2, %5};\n\tmov.b64 b, {%3, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, c;\n\t}" ::"r"(leader),
+      "r"(d_tmem), "r"(a_lo), "r"(b_lo), "r"(idesc), "n"(kDescHi), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+// the same with A in TMEM
+__device__ __forceinline__ void mma_ts(int leader, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, c;\n\t.reg .b64 b;\n\t"
+      "setp.ne.s32 e, %0, 0;\n\tsetp.ne.b32 c, %6, 0;\n\t"
+      "mov.b64 b, {%3, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], b, %4, c;\n\t}" ::"r"(leader),
+      "r"(d_tmem), "r"(a_tmem), "r"(b_lo), "r"(idesc), "n"(kDescHi), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(int leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.s32 e, %0, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(
+          leader),
+      "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
@@ -163,7 +199,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
   __shared__ int s_abort;
   __shared__ uint32_t s_mask[kXMasks];  // boxes of the key tile that are on pages of the pool
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   pdl_wait();
   pdl_trigger();
   const Unit u = unit_of(p, g);
@@ -200,7 +237,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     mbar_init(q_full, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 128);
+      mbar_init(&p_full[s], 4);
       mbar_init(&o_done[s], 1);
     }
     fence_mbar_init();
@@ -280,39 +317,41 @@ __global__ void __launch_bounds__(kXThreads, 1)
     // ----------------------------------------------------------------------- MMA issuer
     constexpr uint32_t idS = tc::idesc_bf16(128, 128, false, false);
     constexpr uint32_t idO = tc::idesc_bf16(128, D, false, true);
+    const int leader = elect_one();
+    const uint32_t ring = smem_u32(smem + L::kRing), empty0 = smem_u32(empty);
+    const uint32_t q_lo = desc_lo(smem_u32(smem + L::kQ), 16);
+    const uint32_t q_next = wide ? L::kTile >> 4 : 0;  // to the second stream's queries
     auto ready = [&](int k) {
       return __all_sync(0xffffffffu,
                         mbar_wait_bounded(&full[k % L::kSlots], (k / L::kSlots) & 1));
     };
     // S_s of the stream's step i
     auto issue_s = [&](int s, int i) -> bool {
-      const int k = 2 * tile_at(s, i);
+      const int k = 2 * tile_at(s, i), sl = k % L::kSlots;
       if (!ready(k)) return false;
-      if (lane == 0) {
-        tc::fence_after_sync();
-        const unsigned char* q = smem + L::kQ + (wide ? s : 0) * L::kTile;
-        const unsigned char* kt = slot_at(k % L::kSlots);
+      tc::fence_after_sync();
+      const uint32_t a = q_lo + (s ? q_next : 0), b = desc_lo(ring + sl * L::kTile, 16);
+      const uint32_t d = s_col(s);
+      mma_ss<false>(leader, d, a, b, idS);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const int at = (kk >> 2) * 16384 + (kk & 3) * 32;
-          tc::mma_f16_ss(s_col(s), tc::smem_desc_sw128(q + at, 16, 1024),
-                         tc::smem_desc_sw128(kt + at, 16, 1024), idS, kk > 0);
-        }
-        tc::mma_commit(&s_full[s]);
-        if (!wide || s == 1) tc::mma_commit(&empty[k % L::kSlots]);
+      for (int kk = 1; kk < D / 16; ++kk) {
+        const uint32_t at = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+        mma_ss<true>(leader, d, a + at, b + at, idS);
       }
-      __syncwarp();
+      commit_one(leader, smem_u32(&s_full[s]));
+      if (!wide || s == 1) commit_one(leader, empty0 + 8 * sl);
       return true;
     };
     bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_full, 0));
     for (int s = 0; s < 2 && ok; ++s)
       if (steps(s) > 0) ok = issue_s(s, 0);
     for (int i = 0; i < steps(0) && ok; ++i) {
-      for (int s = 0; s < 2 && ok; ++s) {
-        if (i >= steps(s)) continue;
-        const int ti = tile_at(s, i), k = 2 * ti + 1;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!ok || i >= steps(s)) continue;
+        const int ti = tile_at(s, i), k = 2 * ti + 1, sl = k % L::kSlots;
         ok = ready(k);
-        if (!ok) break;
+        if (!ok) continue;
         // rows of V without a key, once per tile
         if (!wide || s == 0) {
           const int t = u.tile0 + ti;
@@ -320,7 +359,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
           const int left = (own ? u.n1 : u.n0) - (own ? t - u.tiles0 : t) * kXKeys;
           const uint32_t have = s_mask[ti % kXMasks];
           if (left < kXKeys || have != all_boxes) {
-            unsigned char* vt = slot_at(k % L::kSlots);
+            unsigned char* vt = slot_at(sl);
             for (int r = lane; r < kXKeys; r += 32) {
               if (r < left && ((have >> (r >> g.box_shift)) & 1)) continue;
               for (int hf = 0; hf < kHalves; ++hf)
@@ -334,26 +373,22 @@ __global__ void __launch_bounds__(kXThreads, 1)
           }
         }
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&p_full[s], i & 1));
-        if (!ok) break;
-        if (lane == 0) {
-          tc::fence_after_sync();
-          const unsigned char* vt = slot_at(k % L::kSlots);
+        if (!ok) continue;
+        tc::fence_after_sync();
+        const uint32_t b = desc_lo(ring + sl * L::kTile, 16384);
+        mma_ts(leader, o_col(s), s_col(s), b, idO, i > 0);
 #pragma unroll
-          for (int kk = 0; kk < kXKeys / 16; ++kk)
-            mma_f16_ts(o_col(s), s_col(s) + kk * 8,
-                       tc::smem_desc_sw128(vt + kk * 2048, 16384, 1024), idO,
-                       (i > 0 || kk > 0) ? 1u : 0u);
-          if (!wide || s == 1) tc::mma_commit(&empty[k % L::kSlots]);
-          if (i + 1 == steps(s)) tc::mma_commit(&o_done[s]);
-        }
-        __syncwarp();
-        if (i + 1 < steps(s)) ok = issue_s(s, i + 1);
+        for (int kk = 1; kk < kXKeys / 16; ++kk)
+          mma_ts(leader, o_col(s), s_col(s) + kk * 8, b + kk * (2048 >> 4), idO, 1u);
+        if (!wide || s == 1) commit_one(leader, empty0 + 8 * sl);
+        if (i + 1 == steps(s)) commit_one(leader, smem_u32(&o_done[s]));
+        else ok = issue_s(s, i + 1);
       }
     }
     if (!ok && lane == 0) s_abort = 1;
     // every MMA issued has completed before TMEM and shared memory are given up
-    if (lane == 0 && !ok) {
-      tc::mma_commit(q_full);
+    if (!ok) {
+      commit_one(leader, smem_u32(q_full));
       (void)mbar_wait_bounded(q_full, 1);
     }
   }
@@ -447,7 +482,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
       l = l * corr + (((sl[0] + sl[1]) + (sl[2] + sl[3])) + ((sl[4] + sl[5]) + (sl[6] + sl[7])));
       tc::tmem_wait_st();
       tc::fence_before_sync();
-      mbar_arrive(&p_full[s]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[s]);
     }
     if (ok && ns > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&o_done[s], 0));
     if (!ok) {

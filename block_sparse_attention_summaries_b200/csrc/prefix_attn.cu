@@ -254,31 +254,37 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p)
     // tokens beyond max_q of their request were not attended
     if (b >= p.B || t - p.cu_q[b] >= p.max_q) return;
   }
-  // the row's pieces: dense ones, then up to two runs of item slots
-  int first[2] = {0, 0}, count[2] = {0, 0}, at[2] = {0, 0};
+  // the row's pieces: dense ones, then up to two runs of item slots (first row, rows from one to
+  // the next, how many)
+  long long first0 = 0, first1 = 0;
+  int count0 = 0, count1 = 0;
   if (p.item_ctas) {
-    const int h = hq >> p.g_shift, g = hq - h * p.G;
-    auto pieces = [&](int k, int item, int r) {
+    const int h = hq >> p.g_shift, g = hq & (p.G - 1);
+    auto pieces = [&](int item, int r, long long& first, int& count) {
       const int2 c = p.item_cta[item];  // cut: a run that stopped early has not written it
       const int c0 = min(max(c.x, 0), p.item_ctas - 1), c1 = min(max(c.y, c0), p.item_ctas - 1);
-      first[k] = item + c0;
-      count[k] = c1 - c0 + 1;
-      at[k] = r;
+      first = pa_item_row(p, item, c0) + r;
+      count = c1 - c0 + 1;
     };
-    if (p.prefix_items) pieces(0, h, t * p.G + g);
+    if (p.prefix_items) {
+      const int groups = p.prefix_items / p.Hk, r = (t << p.g_shift) + g;
+      const int at = r / p.prefix_rows;  // its group
+      pieces(h * groups + at, r - at * p.prefix_rows, first0, count0);
+    }
     const PaRequest r = pa_request(p, b);
-    if (pa_own_keys(p, r) > 0) pieces(1, p.prefix_items + b * p.Hk + h, (t - r.t0) * p.G + g);
+    if (pa_own_keys(p, r) > 0)
+      pieces(p.prefix_items + b * p.Hk + h, ((t - r.t0) << p.g_shift) + g, first1, count1);
   }
-  const int ns = p.ns1 + p.ns2, n = ns + count[0] + count[1];
+  const int ns = p.ns1 + p.ns2, n = ns + count0 + count1;
   auto piece = [&](int s, const float2*& ml, const float*& o) {
     if (s < ns) {
       const long long i = s * rows + row;
       ml = p.part_ml + i;
       o = p.part_o + i * D;
     } else {
-      const int k = s - ns < count[0] ? 0 : 1;
-      const long long i =
-          (long long)(first[k] + s - ns - (k ? count[0] : 0)) * p.item_rows + at[k];
+      const int e = s - ns;
+      const long long i = e < count0 ? first0 + (long long)e * p.prefix_rows
+                                     : first1 + (long long)(e - count0) * p.own_rows;
       ml = p.item_ml + i;
       o = p.item_o + i * D;
     }
@@ -342,6 +348,10 @@ int pieces_for(long long units, long long ctas, long long tiles) {
 }
 
 constexpr int kRowsCtas = 2 * kSMs;  // of the few-rows kernel: two per SM
+constexpr int kRowsMax = 64;         // its rows
+// Key tiles of 32 KB (over all heads and row groups) up to which the few-rows kernel takes the prefix of
+// more rows: four a CTA.
+constexpr long long kPrefixTiles = 4 * kRowsCtas;
 
 // Which kernel does which part.
 struct PrefixPlan {
@@ -349,8 +359,8 @@ struct PrefixPlan {
   int simt1, simt2;        // its row tiles: packed (prefix), of a request (own keys); 0: not its part
   int tc1, tc2;            // 256-row tiles on the tensor cores, the same way
   bool fused, direct;      // request tiles take the prefix too; one piece in all, no merge
-  bool rows, rows_prefix;  // own keys (and the prefix) as items of the few-rows kernel
-  int ns1, ns2, item_rows;
+  int mt, groups;          // few-rows kernel: 16-row tiles (0: not used), row groups of the prefix
+  int ns1, ns2, prefix_rows, own_rows;
   long long items;
   size_t ml_bytes, o_bytes, cta_bytes, item_ml_bytes, item_o_bytes;
   size_t bytes() const { return ml_bytes + o_bytes + cta_bytes + item_ml_bytes + item_o_bytes; }
@@ -364,21 +374,30 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
   const long long keys2 = (long long)table_ld * page;
   w.rg = rows_q <= 16 ? 16 : 64;
   auto tiles = [](long long n, int of) { return (int)((n + of - 1) / of); };
-  if (dt == BSA_BF16 && rows_q > 16) {
-    // A request with more than 16 rows: 128-row tiles on the tensor cores.  Requests that fill half
+  auto mt_of = [](long long n) { return n <= 16 ? 1 : n <= 32 ? 2 : 4; };
+  if (dt == BSA_BF16 && rows_q > kRowsMax) {
+    // A request with more than 64 rows: 128-row tiles on the tensor cores.  Requests that fill half
     // a tile on average keep their rows to themselves: prefix and own keys in one pass.  Below that
     // the padding would cost more than the merge.
     w.fused = rows >= 64LL * B;
     w.tc2 = tiles(rows_q, 256);
     if (!w.fused && prefix_len) w.tc1 = tiles(rows, 256);
   } else if (dt == BSA_BF16) {
-    // Up to 16 rows share a key: the few-rows kernel; it takes the prefix too while all rows of a kv
-    // head fit its 16, else they fill 128-row tiles.
-    w.rows = true;
-    w.rows_prefix = prefix_len && rows <= 16;
-    if (prefix_len && !w.rows_prefix) w.tc1 = tiles(rows, 256);
-    w.item_rows = (int)(w.rows_prefix ? std::max(rows, rows_q) : rows_q);
-    w.items = (w.rows_prefix ? Hk : 0) + (long long)B * Hk;
+    // Up to 64 rows share an own key: the few-rows kernel.  It takes the prefix too where all rows
+    // of a kv head fit its tile, or where reading the prefix once per row group is cheap; else the
+    // rows of all requests fill 128-row tiles.
+    w.mt = mt_of(rows_q);
+    if (prefix_len && rows <= kRowsMax) {
+      w.mt = std::max(w.mt, mt_of(rows));
+      w.groups = 1;
+    } else if (prefix_len) {
+      const int groups = tiles(rows, 16 * w.mt);
+      if ((long long)groups * Hk * tiles(prefix_len, 8192 / d) <= kPrefixTiles) w.groups = groups;
+      else w.tc1 = tiles(rows, 256);
+    }
+    w.prefix_rows = 16 * w.mt;
+    w.own_rows = (int)rows_q;
+    w.items = ((long long)w.groups + B) * Hk;
   } else {
     w.simt1 = prefix_len ? tiles(rows, w.rg) : 0;
     w.simt2 = keys2 ? tiles(rows_q, w.rg) : 0;
@@ -393,11 +412,12 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
   const long long all = w.direct ? 0 : (long long)T * Hq * (w.ns1 + w.ns2);
   w.ml_bytes = align_up((size_t)all * sizeof(float2), 256);
   w.o_bytes = align_up((size_t)all * d * sizeof(float), 256);
-  if (w.rows) {
-    const size_t slots = (size_t)(w.items + kRowsCtas) * w.item_rows;
+  if (w.mt) {
+    const size_t n = (w.groups ? ((size_t)w.groups * Hk + kRowsCtas) * w.prefix_rows : 0) +
+                     ((size_t)B * Hk + kRowsCtas) * w.own_rows;
     w.cta_bytes = align_up((size_t)w.items * sizeof(int2), 256);
-    w.item_ml_bytes = align_up(slots * sizeof(float2), 256);
-    w.item_o_bytes = slots * d * sizeof(float);
+    w.item_ml_bytes = align_up(n * sizeof(float2), 256);
+    w.item_o_bytes = n * d * sizeof(float);
   }
   return w;
 }
@@ -422,8 +442,8 @@ bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status,
   if constexpr (sizeof(T) == 2) {
     const bsa_status rc = prefix_attn_tc(p, D, w.tc1, w.tc2, w.fused, w.direct, status, st);
     if (rc != BSA_OK || w.direct) return rc;
-    if (w.rows) {
-      const bsa_status rr = prefix_attn_rows(p, D, w.rows_prefix, w.tc1 > 0, status, st);
+    if (w.mt) {
+      const bsa_status rr = prefix_attn_rows(p, D, w.mt, w.groups, w.tc1 > 0, status, st);
       if (rr != BSA_OK) return rr;
     }
   }
@@ -509,9 +529,10 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
   p.item_ml = reinterpret_cast<float2*>(ws += w.cta_bytes);
   p.item_o = reinterpret_cast<float*>(ws += w.item_ml_bytes);
   p.ns1 = w.ns1; p.ns2 = w.ns2;
-  p.item_rows = w.item_rows;
-  p.item_ctas = w.rows ? kRowsCtas : 0;
-  p.prefix_items = w.rows_prefix ? Hk : 0;
+  p.prefix_rows = w.prefix_rows;
+  p.own_rows = w.own_rows;
+  p.item_ctas = w.mt ? kRowsCtas : 0;
+  p.prefix_items = w.groups * Hk;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dt == BSA_BF16)
     return d == 64 ? launch_parts<__nv_bfloat16, 64>(p, w, status, st)

@@ -30,13 +30,13 @@ struct PrefixParams {
   float* part_o;
   float2* part_ml;
   int ns1, ns2;
-  // Pieces of prefix_attn_rows: item = kv head of the prefix (the first prefix_items), then request *
-  // Hk + kv head; item_cta[item] = first and last CTA that worked on it; the piece of CTA c is slot
-  // item + c of item_o [slot][item_rows][d] and item_ml [slot][item_rows].
+  // Pieces of prefix_attn_rows: items are the prefix_items = Hk * groups of packed rows x prefix, then
+  // request * Hk + kv head; item_cta[item] = first and last CTA that worked on it; the piece of CTA
+  // c is slot item + c, of prefix_rows rows for a prefix item and own_rows for another (pa_item_row).
   int2* item_cta;
-  float* item_o;
-  float2* item_ml;
-  int item_rows, item_ctas, prefix_items;  // item_ctas = 0: no items
+  float* item_o;    // [row][d]
+  float2* item_ml;  // [row]
+  int prefix_rows, own_rows, item_ctas, prefix_items;  // item_ctas = 0: no items
 };
 
 // Request b: its first new token, how many it has, its own tokens.  Values that would reach
@@ -59,6 +59,12 @@ __device__ __forceinline__ PaRequest pa_request(const PrefixParams& p, int b) {
 // Own keys of a request that any of its new tokens sees.
 __device__ __forceinline__ int pa_own_keys(const PrefixParams& p, const PaRequest& r) {
   return r.nq > 0 ? max(0, r.len - r.nq + min(r.nq, p.max_q)) : 0;
+}
+// First row of the piece that CTA c has of an item.
+__device__ __forceinline__ long long pa_item_row(const PrefixParams& p, int item, int c) {
+  if (item < p.prefix_items) return (long long)(item + c) * p.prefix_rows;
+  return (long long)(p.prefix_items ? p.prefix_items + p.item_ctas : 0) * p.prefix_rows +
+         (long long)(item - p.prefix_items + c) * p.own_rows;
 }
 // New tokens in all: rows at or after this are left as they were.
 __device__ __forceinline__ int pa_tokens(const PrefixParams& p) {
@@ -124,7 +130,7 @@ bsa_status prefix_attn_tc(const PrefixParams& p, int d, int tiles1, int tiles2, 
                           bool direct, int* status, cudaStream_t st);
 
 // prefix_attn_rows.cu
-bsa_status prefix_attn_rows(const PrefixParams& p, int d, bool prefix, bool after_tc, int* status,
-                            cudaStream_t st);
+bsa_status prefix_attn_rows(const PrefixParams& p, int d, int mt, int groups, bool after_tc,
+                            int* status, cudaStream_t st);
 
 }  // namespace bsa

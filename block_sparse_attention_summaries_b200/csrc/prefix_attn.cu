@@ -385,16 +385,14 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
   } else if (dt == BSA_BF16) {
     // Up to 64 rows share an own key: the few-rows kernel.  It takes the prefix too where all rows
     // of a kv head fit its tile, or where reading the prefix once per row group is cheap; else the
-    // rows of all requests fill 128-row tiles.
+    // rows of all requests fill 128-row tiles (32 rows of d = 64 behind 64K keys: 80 us there, 87 us
+    // with 32-row tiles here, whose warps wait for one another more than for HBM).
     w.mt = mt_of(rows_q);
-    if (prefix_len && rows <= kRowsMax) {
-      w.mt = std::max(w.mt, mt_of(rows));
-      w.groups = 1;
-    } else if (prefix_len) {
-      const int groups = tiles(rows, 16 * w.mt);
-      if ((long long)groups * Hk * tiles(prefix_len, 8192 / d) <= kPrefixTiles) w.groups = groups;
-      else w.tc1 = tiles(rows, 256);
-    }
+    const int groups = prefix_len ? tiles(rows, 16 * w.mt) : 0;
+    if (groups <= 1 || (long long)groups * Hk * tiles(prefix_len, 8192 / d) <= kPrefixTiles)
+      w.groups = groups;
+    else
+      w.tc1 = tiles(rows, 256);
     w.prefix_rows = 16 * w.mt;
     w.own_rows = (int)rows_q;
     w.items = ((long long)w.groups + B) * Hk;

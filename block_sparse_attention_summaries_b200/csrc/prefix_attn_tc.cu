@@ -39,6 +39,9 @@ constexpr int kXThreads = 384;
 constexpr int kXRegsSoftmax = 216, kXRegsHelper = 72;
 constexpr int kXKeys = 128;
 constexpr float kXRescale = 8.f;  // log2 units
+// P goes to the tensor cores in two parts: the product with V of the first kXFirst keys runs while
+// the last exponentials are computed
+constexpr int kXFirst = 64;
 constexpr int kXMasks = 8;        // key tiles whose page masks are kept: more than the ring holds
 
 template <int D>
@@ -187,14 +190,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_align1024(smem_raw);
-  __shared__ __align__(8) uint64_t bars[2 * L::kSlots + kXMasks + 7];
+  __shared__ __align__(8) uint64_t bars[2 * L::kSlots + kXMasks + 9];
   uint64_t* full = bars;
   uint64_t* empty = full + L::kSlots;
   uint64_t* mask_full = empty + L::kSlots;  // page mask of a key tile written
   uint64_t* q_full = mask_full + kXMasks;
   uint64_t* s_full = q_full + 1;  // [2]
-  uint64_t* p_full = s_full + 2;  // [2]
-  uint64_t* o_done = p_full + 2;  // [2]
+  uint64_t* p_full = s_full + 2;  // [stream][part]
+  uint64_t* o_done = p_full + 4;  // [2]
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ uint32_t s_mask[kXMasks];  // boxes of the key tile that are on pages of the pool
@@ -237,7 +240,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
     mbar_init(q_full, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 4);
+      mbar_init(&p_full[2 * s], 4);
+      mbar_init(&p_full[2 * s + 1], 4);
       mbar_init(&o_done[s], 1);
     }
     fence_mbar_init();
@@ -372,25 +376,27 @@ __global__ void __launch_bounds__(kXThreads, 1)
             __syncwarp();
           }
         }
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&p_full[s], i & 1));
-        if (!ok) continue;
-        tc::fence_after_sync();
         const uint32_t b = desc_lo(ring + sl * L::kTile, 16384);
-        mma_ts(leader, o_col(s), s_col(s), b, idO, i > 0);
 #pragma unroll
-        for (int kk = 1; kk < kXKeys / 16; ++kk)
-          mma_ts(leader, o_col(s), s_col(s) + kk * 8, b + kk * (2048 >> 4), idO, 1u);
+        for (int part = 0; part < 2; ++part) {
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&p_full[2 * s + part], i & 1));
+          if (!ok) break;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int kk = part ? kXFirst / 16 : 0; kk < (part ? kXKeys : kXFirst) / 16; ++kk)
+            mma_ts(leader, o_col(s), s_col(s) + kk * 8, b + kk * (2048 >> 4), idO, i + kk > 0);
+        }
+        if (!ok) continue;
         if (!wide || s == 1) commit_one(leader, empty0 + 8 * sl);
         if (i + 1 == steps(s)) commit_one(leader, smem_u32(&o_done[s]));
         else ok = issue_s(s, i + 1);
       }
     }
+    // Every product issued is complete, and every arrival that waits for one is made, before TMEM and
+    // shared memory are given up: an arrival behind the CTA's end would hit the next CTA's barriers.
+    commit_one(leader, smem_u32(q_full));
+    ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_full, 1)) && ok;
     if (!ok && lane == 0) s_abort = 1;
-    // every MMA issued has completed before TMEM and shared memory are given up
-    if (!ok) {
-      commit_one(leader, smem_u32(q_full));
-      (void)mbar_wait_bounded(q_full, 1);
-    }
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kXRegsSoftmax));
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       const uint64_t sc2 = tc::pack_f2(scale, scale), nm2 = tc::pack_f2(neg_m, neg_m);
       uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-      for (int c = 0; c < 128; c += 32) {
+      for (int c = 0; c < kXKeys; c += 32) {
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -475,6 +481,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
           pk[e / 2] = *reinterpret_cast<const uint32_t*>(&b2);
         }
         tmem_st16(s_col(s) + lanes + c / 2, pk);
+        if (c + 32 == kXFirst) {
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * s]);
+        }
       }
       float sl[8];
 #pragma unroll
@@ -483,7 +495,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[s]);
+      if (lane == 0) mbar_arrive(&p_full[2 * s + 1]);
     }
     if (ok && ns > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&o_done[s], 0));
     if (!ok) {
@@ -492,78 +504,83 @@ __global__ void __launch_bounds__(kXThreads, 1)
       l = NAN;
     }
     tc::fence_after_sync();
-    // deep units: the second stream's half joins through shared memory (the ring: both
-    // streams' products are complete behind the first barrier)
-    float w = 1.f;
-    unsigned char* xch = smem + L::kRing;
-    auto at = [&](int c4) { return xch + (r * (D / 4) + (c4 ^ (r & (D / 4 - 1)))) * 16; };
+    // O to memory through shared memory, so that a warp writes whole rows (a thread writing its own
+    // row 16 bytes at a time took 4.4 us a unit).  A deep unit's streams join their halves: TMEM lanes
+    // are the rows for both, so each stream's warps read both O and write half the columns.
+    float w0 = 1.f, w1 = 0.f;
+    unsigned char* stage = smem + L::kQ + s * L::kTile + (warp & 3) * (L::kTile / 4);
     if (!wide) {
       float2* ml = reinterpret_cast<float2*>(smem + L::kQ + L::kTile);  // no second query tile
       ml[s * 128 + r] = make_float2(m, l);
+      tc::fence_before_sync();
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float2 other = ml[(s ^ 1) * 128 + r];
-      const float top = fmaxf(m, other.x);
-      const float base = top == -INFINITY ? 0.f : top;
-      w = tc::ex2_approx(m - base);
-      if (s == 1 && ns > 0) {
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          float ov[32];
-          tc::tmem_ld32(o_col(1) + lanes + c, ov);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(at((c + e) / 4)) =
-                make_float4(ov[e] * w, ov[e + 1] * w, ov[e + 2] * w, ov[e + 3] * w);
-        }
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      l = l * w + other.y * tc::ex2_approx(other.x - base);
-      m = top;
+      tc::fence_after_sync();
+      const float2 a = ml[r], b = ml[128 + r];
+      m = fmaxf(a.x, b.x);
+      const float base = m == -INFINITY ? 0.f : m;
+      w0 = tc::ex2_approx(a.x - base);
+      w1 = tc::ex2_approx(b.x - base);
+      l = a.y * w0 + b.y * w1;
+      stage = smem + L::kRing + warp * (L::kTile / 4);  // both streams have read the ring
     }
-    if (wide || s == 0) {
-      const bool join = !wide && nt > 1;
-      const bool live = row < u.nrows;
-      const long long id = live ? row_id(row) : 0;
-      const float inv = !g.direct ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      if (live) {
-        if (!g.direct) p.part_ml[u.slot * rows + id] = make_float2(m, l);
-        else if (p.lse) p.lse[id] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPaLn2;
-      }
+    const bool live = row < u.nrows;
+    if (live && (wide || s == 0)) {
+      const long long id = row_id(row);
+      if (!g.direct) p.part_ml[u.slot * rows + id] = make_float2(m, l);
+      else if (p.lse) p.lse[id] = l == 0.f ? -INFINITY : (m + log2f(l)) * kPaLn2;
+    }
+    if (g.direct) {
+      const float inv = 1.f / l;  // a row without a key is set to 0 below
+      w0 *= inv;
+      w1 *= inv;
+    }
+    constexpr int PC = D / 2;  // columns of a pass: 32 rows of them fill the warp's share of a tile
+    const int row0 = (warp & 3) * 32 + (wide ? 128 * s : 0);  // the warp's first row
+    for (int pass = 0; pass < (wide ? 2 : 1); ++pass) {
+      const int col = (wide ? pass : s) * PC;
 #pragma unroll
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < PC; c += 32) {
         float ov[32];
-        tc::tmem_ld32(o_col(s) + lanes + c, ov);
+        tc::tmem_ld32(o_col(wide ? s : 0) + lanes + col + c, ov);
         tc::tmem_wait_ld();
+        tc::reg_fence(ov);
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          float4 o4 = make_float4(ov[e] * w, ov[e + 1] * w, ov[e + 2] * w, ov[e + 3] * w);
-          if (join) {
-            const float4 x4 = *reinterpret_cast<const float4*>(at((c + e) / 4));
-            o4 = make_float4(o4.x + x4.x, o4.y + x4.y, o4.z + x4.z, o4.w + x4.w);
-          }
-          ov[e] = o4.x; ov[e + 1] = o4.y; ov[e + 2] = o4.z; ov[e + 3] = o4.w;
+        for (int e = 0; e < 32; ++e) ov[e] *= w0;
+        if (!wide && nt > 1) {
+          float o1[32];
+          tc::tmem_ld32(o_col(1) + lanes + col + c, o1);
+          tc::tmem_wait_ld();
+          tc::reg_fence(o1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = fmaf(o1[e], w1, ov[e]);
         }
-        if (!live) continue;
+        if (l == 0.f)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(stage + lane * (PC * 4) +
+                                     ((((c + e) >> 2) ^ (lane & (PC / 4 - 1))) << 4)) =
+              make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+      }
+      __syncwarp();
+      constexpr int LR = PC / 4;  // lanes of a row, 16 bytes each
+#pragma unroll 4
+      for (int i = 0; i < 32; i += 32 / LR) {
+        const int rr = i + lane / LR, ch = lane % LR;
+        const float4 v = *reinterpret_cast<const float4*>(stage + rr * (PC * 4) +
+                                                          ((ch ^ (rr & (LR - 1))) << 4));
+        if (row0 + rr >= u.nrows) continue;
+        const long long id = row_id(row0 + rr);
         if (g.direct) {
-          __nv_bfloat16* op = static_cast<__nv_bfloat16*>(p.o) + id * D + c;
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            __nv_bfloat162 b2[4];
-#pragma unroll
-            for (int f = 0; f < 4; ++f)  // a row without a key: 0, not what TMEM holds
-              b2[f] = __floats2bfloat162_rn(l == 0.f ? 0.f : ov[e + 2 * f] * inv,
-                                            l == 0.f ? 0.f : ov[e + 2 * f + 1] * inv);
-            *reinterpret_cast<uint4*>(op + e) = *reinterpret_cast<uint4*>(b2);
-          }
+          __nv_bfloat162 b2[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + id * D + col + 4 * ch) =
+              *reinterpret_cast<uint2*>(b2);
         } else {
-          float* op = p.part_o + (u.slot * rows + id) * D + c;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(op + e) =
-                make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+          *reinterpret_cast<float4*>(p.part_o + (u.slot * rows + id) * D + col + 4 * ch) = v;
         }
       }
+      __syncwarp();
     }
   }
   tc::fence_before_sync();

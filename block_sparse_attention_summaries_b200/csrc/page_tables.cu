@@ -10,7 +10,8 @@
 // pool that runs dry refuses whole requests, in order, never half of one), and takes ring entries
 // G_b - grow_b .. G_b - 1 behind head.  A shrinking request's pages go to the ring's end in request
 // order.  Token t of the packed new tokens belongs to the request whose range of the exclusive sum
-// of new tokens holds it, found by a binary search in shared memory.  All integer work on a few KB:
+// of new tokens holds it, found by a binary search in shared memory unless the 128 tokens of a warp
+// step all belong to the request before; a page that moves finds its request the same way.  All integer work on a few KB:
 // what bounds it is latency (the lengths' load, a block scan, the dependent page-id load), so it is
 // ONE launch: a cluster of up to 8 CTAs, each of which scans all requests for itself (one load and
 // a scan are cheaper than a second launch or a grid-wide exchange) and then handles its share of
@@ -78,7 +79,7 @@ __device__ __forceinline__ int ring_at(int head, int off, int N) {
   return i >= N ? i - N : i;
 }
 
-__global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTablesParams p) {
+__global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTablesParams p) {
   extern __shared__ int sm[];
   int* s_cu = sm;                  // [B + 1] first new token of the request
   int* s_len = s_cu + p.B + 1;     // [B] tokens before; -1: not served, its tokens get no slot
@@ -168,71 +169,82 @@ __global__ void __launch_bounds__(kPtThreads) page_tables_kernel(const PageTable
   const int freed = (int)min(s_freed, (long long)(p.N - avail));
   if (tid == 0 && s_freed > freed) atomicOr(&s_bits, BSA_PAGES_RING);
 
-  // pages that join and leave: a lane per request, together for one that moves many
-  for (int b0 = (rank * warps + warp) * 32; b0 < p.B; b0 += ranks * threads) {
-    const int b = b0 + lane;
-    Ask a = {0, 0, 0, true};
-    if (b < p.B) {
-      p.cu_new[b] = s_cu[b];
-      p.lens_out[b] = s_new[b];
-      if (s_len[b] >= 0) a = ask(p, s_len[b], s_new[b]);
+  const int all = ranks * threads, me = rank * threads + tid;
+  for (int b = me; b < p.B; b += all) {
+    p.cu_new[b] = s_cu[b];
+    p.lens_out[b] = s_new[b];
+  }
+  // the last entry of s[0 .. B) that is at most x (s ascends, s[0] = 0): of the requests whose ranges
+  // start there, the last is the one that has any
+  auto owner = [&](const int* s, int lo, int x) {
+    int hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s[mid] <= x) lo = mid; else hi = mid;
     }
-    const int moves = abs(a.want - a.have);
-    auto move = [&](int req, int have, int want, int i) {
-      int* row = p.table + (size_t)req * p.ld;
-      if (want > have) {
-        row[have + i] = p.ring[ring_at(head, s_take[req] + i, p.N)];
-      } else {
-        const long long off = (long long)s_drop[req] + i;
-        if (off < freed) p.ring[ring_at(head, avail + (int)off, p.N)] = row[want + i];
-      }
-    };
-    if (moves == 1) move(b, a.have, a.want, 0);
-    for (uint32_t many = __ballot_sync(0xffffffffu, moves > 1); many; many &= many - 1) {
-      const int src = __ffs(many) - 1;
-      const int have = __shfl_sync(0xffffffffu, a.have, src);
-      const int want = __shfl_sync(0xffffffffu, a.want, src);
-      for (int i = lane; i < abs(want - have); i += 32) move(b0 + src, have, want, i);
-    }
+    return lo;
+  };
+  // pages that join and pages that leave, one after another over all threads
+  const int page_mask = (1 << p.page_shift) - 1;
+  auto pages_of = [&](int n) { return (int)(((long long)n + page_mask) >> p.page_shift); };
+  for (int i = me; i < (int)s_taken; i += all) {
+    const int b = owner(s_take, 0, i);
+    p.table[(size_t)b * p.ld + pages_of(s_len[b]) + (i - s_take[b])] = p.ring[ring_at(head, i, p.N)];
+  }
+  for (int i = me; i < freed; i += all) {
+    const int b = owner(s_drop, 0, i);
+    p.ring[ring_at(head, avail + i, p.N)] =
+        p.table[(size_t)b * p.ld + pages_of(s_new[b]) + (i - s_drop[b])];
   }
 
-  // slots and positions of the new tokens, four a thread
+  // slots and positions of the new tokens: a run of consecutive tokens per warp, 128 at a time, four
+  // a lane (with one a lane the 8 SMs spent 14 us issuing the instructions of a quarter million)
+  const int gwarp = rank * warps + warp, gwarps = ranks * warps;
   const int total = s_cu[p.B];
-  const int page_mask = (1 << p.page_shift) - 1;
-  for (int t0 = (rank * threads + tid) * 4; t0 < p.max_tokens; t0 += ranks * threads * 4) {
-    int lo = 0;  // the last request whose range starts at or before t0
-    if (t0 < total) {
-      int hi = p.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_cu[mid] <= t0) lo = mid; else hi = mid;
-      }
-    }
-    int slot[4], pos[4];
-    int page_at = -1, page_b = -1, id = -1;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int t = t0 + e;
-      slot[e] = pos[e] = -1;
-      if (t >= total) continue;
-      while (s_cu[lo + 1] <= t) ++lo;
+  const long long run = (((long long)p.max_tokens + gwarps - 1) / gwarps + 127) / 128 * 128;
+  const int t_end = (int)min((long long)p.max_tokens, (gwarp + 1) * run);
+  auto page_id = [&](int b, int len, int c) {
+    const int have = pages_of(len);
+    return c < have ? p.table[(size_t)b * p.ld + c]
+                    : p.ring[ring_at(head, s_take[b] + (c - have), p.N)];
+  };
+  int lo = 0;  // a request whose range starts at or before the warp's tokens
+  for (int w0 = (int)min((long long)p.max_tokens, gwarp * run); w0 < t_end; w0 += 128) {
+    const int t0 = w0 + 4 * lane;
+    int slot[4] = {-1, -1, -1, -1}, pos[4] = {-1, -1, -1, -1};
+    if (w0 + 128 <= s_cu[lo + 1]) {  // all in the request of the tokens before
       const int len = s_len[lo];
-      if (len < 0) continue;
-      const int own = len + (t - s_cu[lo]);
-      const int c = own >> p.page_shift;
-      if (c != page_at || lo != page_b) {
-        const int have = (int)(((long long)len + page_mask) >> p.page_shift);
-        id = c < have ? p.table[(size_t)lo * p.ld + c]
-                      : p.ring[ring_at(head, s_take[lo] + (c - have), p.N)];
-        page_at = c;
-        page_b = lo;
-        if (id < 0 || id >= p.N) {
-          id = -1;
-          if (t < p.max_tokens) atomicOr(&s_bits, BSA_PAGES_BAD_ID);
+      if (len >= 0) {
+        const int own = len + (t0 - s_cu[lo]);
+        const int c = own >> p.page_shift, c3 = (own + 3) >> p.page_shift;
+        int id = page_id(lo, len, c);
+        const int id3 = c3 == c ? id : page_id(lo, len, c3);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = (own + e) >> p.page_shift == c ? id : id3;
+          const bool there = i >= 0 && i < p.N;
+          if (!there && t0 + e < p.max_tokens) atomicOr(&s_bits, BSA_PAGES_BAD_ID);
+          slot[e] = there ? (i << p.page_shift) + ((own + e) & page_mask) : -1;
+          pos[e] = own + e + p.pos_offset;
         }
       }
-      if (id >= 0) slot[e] = (id << p.page_shift) + (own & page_mask);
-      pos[e] = own + p.pos_offset;
+    } else if (w0 < total) {
+      int b = owner(s_cu, lo, min(t0, total - 1));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = t0 + e;
+        if (t >= total) continue;
+        while (s_cu[b + 1] <= t) ++b;
+        const int len = s_len[b];
+        if (len < 0) continue;
+        const int own = len + (t - s_cu[b]);
+        const int i = page_id(b, len, own >> p.page_shift);
+        const bool there = i >= 0 && i < p.N;
+        if (!there && t < p.max_tokens) atomicOr(&s_bits, BSA_PAGES_BAD_ID);
+        slot[e] = there ? (i << p.page_shift) + (own & page_mask) : -1;
+        pos[e] = own + p.pos_offset;
+      }
+      lo = __shfl_sync(0xffffffffu, b, 31);
     }
     if (p.vec4 && t0 + 4 <= p.max_tokens) {
       *reinterpret_cast<int4*>(p.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);

@@ -10,26 +10,29 @@
 // and each request's own keys only for its own rows.  Both parts may be cut into pieces along the
 // keys when there are too few tiles to fill the GPU; prefix_merge_kernel joins a row's pieces.
 //
-// prefix_simt_kernel: any type, CUDA cores.  A CTA of 256 threads takes RG rows (of one kv head,
-// row = token * G + head of the group) and a piece of the keys in tiles of 64: S = Q K^T in
-// registers from shared memory, online softmax with the running maximum and sum of each row in
-// registers of the 16 threads that share it, P through shared memory, O += P V in registers.
+// prefix_simt_kernel: float32, CUDA cores (its tensor-core formats would round q, k and the weights).
+// A CTA of 256 threads takes RG rows (of one kv head, row = token * G + head of the group) and a
+// piece of the keys in tiles of 64 (d = 64) or 32: S = Q K^T in registers from shared memory, online
+// softmax with the running maximum and sum of each row in registers of the 16 threads that share
+// it, P through shared memory, O += P V in registers.  The next tile is copied (cp.async) while one is
+// worked on, its page ids read a tile earlier still: with loads in line a tile took 5 us, the time of
+// two dependent trips to memory.
 #include "prefix_attn.cuh"
 
 namespace bsa {
 namespace {
 
 constexpr int kPsThreads = 256;
-constexpr int kPsKeys = 64;  // keys of a tile
 
 template <int D, int RG>
 struct SimtSmem {
-  static constexpr int kLd = D + 4;  // floats; rows 4 banks apart
-  static constexpr int kLdP = kPsKeys + 4;
+  static constexpr int kKeys = 4096 / D;  // 16 KB of K or V
+  static constexpr int kLd = D + 4;       // floats; rows 4 banks apart
+  static constexpr int kLdP = kKeys + 4;
   static constexpr int kQ = 0;
-  static constexpr int kK = kQ + RG * kLd;
-  static constexpr int kV = kK + kPsKeys * kLd;
-  static constexpr int kP = kV + kPsKeys * kLd;
+  static constexpr int kTile = kKeys * kLd;
+  static constexpr int kKV = kQ + RG * kLd;      // two buffers of K and V
+  static constexpr int kP = kKV + 4 * kTile;
   static constexpr int kTotal = (kP + RG * kLdP) * (int)sizeof(float);
 };
 
@@ -38,138 +41,156 @@ struct SimtGrid {
   int tiles2;  // row tiles of a request
 };
 
-template <typename T, int D, int RG>
-__global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixParams p,
-                                                                 const SimtGrid g) {
-  using L = SimtSmem<D, RG>;
-  constexpr int TM = RG / 16;  // rows of a thread
-  constexpr int DC = D / 64;   // float4 columns of a thread
-  extern __shared__ __align__(16) float smf[];
-  float *sq = smf + L::kQ, *sk = smf + L::kK, *sv = smf + L::kV, *sp = smf + L::kP;
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  pdl_wait();
-  pdl_trigger();
-
-  // the unit: rows r0 .. r0 + nrows of kv head h (row = token * G + head of the group), keys
-  // [0, n) on `pages`; row r sees keys j <= first_pos + r / G
-  int u = blockIdx.x, h, nrows, r0, n, slot, piece, pieces;
-  int first_pos;
+// The rows and keys of a CTA.
+struct SimtUnit {
+  int h, r0, nrows;  // rows r0 .. r0 + nrows of kv head h
+  int n, first_pos;  // keys [0, n) on `pages`; row r sees keys j <= first_pos + r / G
   const int* pages;
-  if (u < g.units1) {
-    piece = u % p.ns1;
-    u /= p.ns1;
-    h = u % p.Hk;
-    r0 = u / p.Hk * RG;
-    nrows = min(RG, pa_tokens(p) * p.G - r0);
-    pages = p.ptable;
-    n = p.prefix_len;
-    first_pos = n;
-    slot = piece;
-    pieces = p.ns1;
-  } else {
-    u -= g.units1;
-    piece = u % p.ns2;
-    u /= p.ns2;
-    h = u % p.Hk;
-    u /= p.Hk;
-    const int tile = u % g.tiles2, b = u / g.tiles2;
-    const PaRequest r = pa_request(p, b);
-    r0 = r.t0 * p.G + tile * RG;
-    nrows = min(RG, min(r.nq, p.max_q) * p.G - tile * RG);
-    pages = p.table + (size_t)b * p.table_ld;
-    // tiles start at whole tokens: G divides RG
-    first_pos = r.len - r.nq + tile * (RG / p.G);
-    n = max(0, min(r.len, first_pos + ((nrows - 1) >> p.g_shift) + 1));
-    slot = p.ns1 + piece;
-    pieces = p.ns2;
-  }
+  int slot, piece, pieces;
+};
+
+// 16 bytes to shared memory behind the back of the thread; `bytes` 0: zeros
+__device__ __forceinline__ void cp_async16(float* dst, const float* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+
+template <int D, int RG>
+__device__ __forceinline__ void simt_unit(const PrefixParams& p, const SimtUnit& un, float* smf) {
+  using L = SimtSmem<D, RG>;
+  constexpr int TM = RG / 16;           // rows of a thread
+  constexpr int NE = L::kKeys / 16;     // keys of a thread's scores
+  constexpr int DC = D / 64;            // float4 columns of a thread
+  constexpr int RPP = kPsThreads / (D / 4);  // key rows copied at a time
+  constexpr int NR = L::kKeys / RPP;         // of each thread
+  float *sq = smf + L::kQ, *sp = smf + L::kP;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int h = un.h, r0 = un.r0, nrows = un.nrows, n = un.n, first_pos = un.first_pos;
+  const int slot = un.slot, piece = un.piece, pieces = un.pieces;
+  const int* pages = un.pages;
   if (nrows <= 0) return;
-  const int tiles = (n + kPsKeys - 1) / kPsKeys, per = (tiles + pieces - 1) / pieces;
+  const int tiles = (n + L::kKeys - 1) / L::kKeys, per = (tiles + pieces - 1) / pieces;
   const int tile0 = min(piece * per, tiles), tile1 = min(tile0 + per, tiles);
 
   const long long rows = (long long)p.T * p.Hq;
   auto row_id = [&](int r) {  // of the partial results: token * Hq + query head
     const int rr = r0 + r;
-    return (long long)((rr >> p.g_shift)) * p.Hq + h * p.G + (rr & (p.G - 1));
+    return (long long)(rr >> p.g_shift) * p.Hq + h * p.G + (rr & (p.G - 1));
   };
-  float m[TM], l[TM], acc[TM][DC * 4];
+  float m[TM], l[TM];
+  uint64_t acc[TM][DC * 2];  // columns tx * 4 + 64 c .. in pairs
 #pragma unroll
   for (int a = 0; a < TM; ++a) {
     m[a] = -INFINITY;
     l[a] = 0.f;
 #pragma unroll
-    for (int c = 0; c < DC * 4; ++c) acc[a][c] = 0.f;
+    for (int c = 0; c < DC * 2; ++c) acc[a][c] = 0ull;
   }
+  // the thread copies 16 bytes (columns 4 cc ..) of rows cr + RPP i of a tile
+  const int cr = tid / (D / 4), cc = tid % (D / 4) * 4;
+  int ids[NR];  // their pages, -1: no key
+  auto read_ids = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int j = tile * L::kKeys + cr + RPP * i;
+      ids[i] = tile < tile1 && j < n ? pages[j >> p.page_shift] : -1;
+    }
+  };
+  auto copy = [&](int tile) {
+    float* dst = smf + L::kKV + (tile & 1) * 2 * L::kTile;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+      const int j = tile * L::kKeys + cr + RPP * i;
+      const bool is = ids[i] >= 0 && ids[i] < p.num_pages;
+      const long long at =
+          is ? (((((long long)ids[i] * p.Hk + h) << p.page_shift) +
+                 (j & ((1 << p.page_shift) - 1))) * D) + cc
+             : 0;
+      cp_async16(dst + (cr + RPP * i) * L::kLd + cc, static_cast<const float*>(p.k) + at,
+                 is ? 16 : 0);
+      cp_async16(dst + L::kTile + (cr + RPP * i) * L::kLd + cc,
+                 static_cast<const float*>(p.v) + at, is ? 16 : 0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   if (tile0 < tile1) {
+    read_ids(tile0);
     // queries, scaled to log2 units
     const float scale = rsqrtf((float)D) * kPaLog2e;
     for (int i = tid; i < RG * (D / 4); i += kPsThreads) {
       const int r = i / (D / 4), c = i % (D / 4) * 4;
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < nrows) {
         const int rr = r0 + r;
-        load_vec<T, 4>(static_cast<const T*>(p.q) + ((rr >> p.g_shift)) * p.q_stride +
-                           (long long)(h * p.G + (rr & (p.G - 1))) * D + c, x);
+        x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) +
+                                             (rr >> p.g_shift) * p.q_stride +
+                                             (long long)(h * p.G + (rr & (p.G - 1))) * D + c);
       }
       *reinterpret_cast<float4*>(sq + r * L::kLd + c) =
-          make_float4(x[0] * scale, x[1] * scale, x[2] * scale, x[3] * scale);
+          make_float4(x.x * scale, x.y * scale, x.z * scale, x.w * scale);
     }
+    copy(tile0);
+    read_ids(tile0 + 1);
   }
   for (int tile = tile0; tile < tile1; ++tile) {
-    const int j0 = tile * kPsKeys;
-    __syncthreads();  // the previous tile is read
-    for (int i = tid; i < kPsKeys * (D / 4); i += kPsThreads) {
-      const int j = i / (D / 4), c = i % (D / 4) * 4;
-      float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-      if (j0 + j < n) {
-        const int id = pages[(j0 + j) >> p.page_shift];
-        if (id >= 0 && id < p.num_pages) {
-          const long long at = (((((long long)id * p.Hk + h) << p.page_shift) +
-                                 ((j0 + j) & ((1 << p.page_shift) - 1))) * D) + c;
-          load_vec<T, 4>(static_cast<const T*>(p.k) + at, x);
-          load_vec<T, 4>(static_cast<const T*>(p.v) + at, y);
-        }
-      }
-      *reinterpret_cast<float4*>(sk + j * L::kLd + c) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(sv + j * L::kLd + c) = make_float4(y[0], y[1], y[2], y[3]);
+    const int j0 = tile * L::kKeys;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // the tile is there, the one before is read
+    if (tile + 1 < tile1) {
+      copy(tile + 1);
+      read_ids(tile + 2);
     }
-    __syncthreads();
-    // scores of keys tx + 16 e
-    float s[TM][4];
+    const float *sk = smf + L::kKV + (tile & 1) * 2 * L::kTile, *sv = sk + L::kTile;
+    // keys tx + 16 e of the tile that exist: in range, on a page of the pool
+    uint32_t live = 0;
 #pragma unroll
-    for (int a = 0; a < TM; ++a)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[a][e] = 0.f;
-#pragma unroll 4
-    for (int c = 0; c < D; c += 4) {
-      float4 kk[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        kk[e] = *reinterpret_cast<const float4*>(sk + (tx + 16 * e) * L::kLd + c);
-#pragma unroll
-      for (int a = 0; a < TM; ++a) {
-        const float4 qq = *reinterpret_cast<const float4*>(sq + (ty * TM + a) * L::kLd + c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[a][e] += qq.x * kk[e].x + qq.y * kk[e].y + qq.z * kk[e].z + qq.w * kk[e].w;
-      }
-    }
-    uint32_t live = 0;  // keys tx + 16 e of the tile that exist: in range, on a page of the pool
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < NE; ++e) {
       const int j = j0 + tx + 16 * e;
       if (j < n) {
         const int id = pages[j >> p.page_shift];
         if (id >= 0 && id < p.num_pages) live |= 1u << e;
       }
     }
+    // scores of keys tx + 16 e, two columns in a packed FMA
+    uint64_t s2[TM][NE];
+#pragma unroll
+    for (int a = 0; a < TM; ++a)
+#pragma unroll
+      for (int e = 0; e < NE; ++e) s2[a][e] = 0ull;
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+      ulonglong2 kk[NE];
+#pragma unroll
+      for (int e = 0; e < NE; ++e)
+        kk[e] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * e) * L::kLd + c);
+#pragma unroll
+      for (int a = 0; a < TM; ++a) {
+        const ulonglong2 qq = *reinterpret_cast<const ulonglong2*>(sq + (ty * TM + a) * L::kLd + c);
+#pragma unroll
+        for (int e = 0; e < NE; ++e)
+          s2[a][e] = tc::fma_f2(qq.y, kk[e].y, tc::fma_f2(qq.x, kk[e].x, s2[a][e]));
+      }
+    }
+    float s[TM][NE];
+#pragma unroll
+    for (int a = 0; a < TM; ++a)
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        float lo, hi;
+        tc::unpack_f2(s2[a][e], lo, hi);
+        s[a][e] = lo + hi;
+      }
+    bool hides = false;  // a row of the thread does not see a key of the tile that exists
 #pragma unroll
     for (int a = 0; a < TM; ++a) {
       const int last = first_pos + ((ty * TM + a) >> p.g_shift);
       float top = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (!((live >> e) & 1) || j0 + tx + 16 * e > last) s[a][e] = -INFINITY;
+      for (int e = 0; e < NE; ++e) {
+        const bool sees = j0 + tx + 16 * e <= last;
+        hides |= !sees && ((live >> e) & 1);
+        if (!((live >> e) & 1) || !sees) s[a][e] = -INFINITY;
         top = fmaxf(top, s[a][e]);
       }
 #pragma unroll
@@ -180,7 +201,7 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
       m[a] = m_new;
       float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < NE; ++e) {
         const float pe = exp2f(s[a][e] - base);
         sp[(ty * TM + a) * L::kLdP + tx + 16 * e] = pe;
         sum += pe;
@@ -189,34 +210,38 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
       for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       l[a] = l[a] * corr + sum;
 #pragma unroll
-      for (int c = 0; c < DC * 4; ++c) acc[a][c] *= corr;
+      for (int c = 0; c < DC * 2; ++c) acc[a][c] = tc::mul_f2(acc[a][c], tc::pack_f2(corr, corr));
     }
-    __syncwarp();  // a row's P is written and read by the 16 threads of its half warp
+    // a row's P is written and read by the 16 threads of its half warp
+    const bool careful = __any_sync(0xffffffffu, hides);
+    auto product = [&](auto check) {
 #pragma unroll 2
-    for (int j = 0; j < kPsKeys; j += 4) {
-      float pj[TM][4];
+      for (int j = 0; j < L::kKeys; j += 4) {
+        float pj[TM][4];
 #pragma unroll
-      for (int a = 0; a < TM; ++a) {
-        const float4 t = *reinterpret_cast<const float4*>(sp + (ty * TM + a) * L::kLdP + j);
-        pj[a][0] = t.x; pj[a][1] = t.y; pj[a][2] = t.z; pj[a][3] = t.w;
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int c = 0; c < DC; ++c) {
-          const float4 vv =
-              *reinterpret_cast<const float4*>(sv + (j + e) * L::kLd + tx * 4 + 64 * c);
-#pragma unroll
-          for (int a = 0; a < TM; ++a) {
-            // a key that the row does not see adds nothing, whatever its value holds
-            const float w = pj[a][e];
-            acc[a][4 * c] = w == 0.f ? acc[a][4 * c] : fmaf(w, vv.x, acc[a][4 * c]);
-            acc[a][4 * c + 1] = w == 0.f ? acc[a][4 * c + 1] : fmaf(w, vv.y, acc[a][4 * c + 1]);
-            acc[a][4 * c + 2] = w == 0.f ? acc[a][4 * c + 2] : fmaf(w, vv.z, acc[a][4 * c + 2]);
-            acc[a][4 * c + 3] = w == 0.f ? acc[a][4 * c + 3] : fmaf(w, vv.w, acc[a][4 * c + 3]);
-          }
+        for (int a = 0; a < TM; ++a) {
+          const float4 t = *reinterpret_cast<const float4*>(sp + (ty * TM + a) * L::kLdP + j);
+          pj[a][0] = t.x; pj[a][1] = t.y; pj[a][2] = t.z; pj[a][3] = t.w;
         }
-    }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < DC; ++c) {
+            const ulonglong2 vv =
+                *reinterpret_cast<const ulonglong2*>(sv + (j + e) * L::kLd + tx * 4 + 64 * c);
+#pragma unroll
+            for (int a = 0; a < TM; ++a) {
+              const float w = pj[a][e];
+              // a key that the row does not see adds nothing, whatever its value holds
+              if (decltype(check)::value && w == 0.f) continue;
+              acc[a][2 * c] = tc::fma_f2(tc::pack_f2(w, w), vv.x, acc[a][2 * c]);
+              acc[a][2 * c + 1] = tc::fma_f2(tc::pack_f2(w, w), vv.y, acc[a][2 * c + 1]);
+            }
+          }
+      }
+    };
+    if (careful) product(std::true_type());
+    else product(std::false_type());
   }
 #pragma unroll
   for (int a = 0; a < TM; ++a) {
@@ -227,8 +252,49 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
     if (l[a] == 0.f) continue;  // no key (scores of NaN leave the maximum at -inf and l at NaN)
 #pragma unroll
     for (int c = 0; c < DC; ++c)
-      *reinterpret_cast<float4*>(p.part_o + at * D + tx * 4 + 64 * c) =
-          make_float4(acc[a][4 * c], acc[a][4 * c + 1], acc[a][4 * c + 2], acc[a][4 * c + 3]);
+      *reinterpret_cast<ulonglong2*>(p.part_o + at * D + tx * 4 + 64 * c) =
+          make_ulonglong2(acc[a][2 * c], acc[a][2 * c + 1]);
+  }
+}
+
+// RG1 rows a tile of the packed rows against the prefix, RG2 of a request against its own keys
+template <int D, int RG1, int RG2>
+__global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixParams p,
+                                                                 const SimtGrid g) {
+  extern __shared__ __align__(16) float smf[];
+  pdl_wait();
+  pdl_trigger();
+  SimtUnit un;
+  int u = blockIdx.x;
+  if (u < g.units1) {
+    un.piece = u % p.ns1;
+    u /= p.ns1;
+    un.h = u % p.Hk;
+    un.r0 = u / p.Hk * RG1;
+    un.nrows = min(RG1, pa_tokens(p) * p.G - un.r0);
+    un.pages = p.ptable;
+    un.n = p.prefix_len;
+    un.first_pos = un.n;
+    un.slot = un.piece;
+    un.pieces = p.ns1;
+    simt_unit<D, RG1>(p, un, smf);
+  } else {
+    u -= g.units1;
+    un.piece = u % p.ns2;
+    u /= p.ns2;
+    un.h = u % p.Hk;
+    u /= p.Hk;
+    const int tile = u % g.tiles2, b = u / g.tiles2;
+    const PaRequest r = pa_request(p, b);
+    un.r0 = r.t0 * p.G + tile * RG2;
+    un.nrows = min(RG2, min(r.nq, p.max_q) * p.G - tile * RG2);
+    un.pages = p.table + (size_t)b * p.table_ld;
+    // tiles start at whole tokens: G divides RG2
+    un.first_pos = r.len - r.nq + tile * (RG2 / p.G);
+    un.n = max(0, min(r.len, un.first_pos + ((un.nrows - 1) >> p.g_shift) + 1));
+    un.slot = p.ns1 + un.piece;
+    un.pieces = p.ns2;
+    simt_unit<D, RG2>(p, un, smf);
   }
 }
 
@@ -341,10 +407,11 @@ __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p)
   if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kPaLn2;
 }
 
-// How the keys are cut: enough pieces that `units` CTAs a piece fill `ctas`, none under 4 tiles.
-int pieces_for(long long units, long long ctas, long long tiles) {
+// How the keys are cut: enough pieces that `units` CTAs a piece fill `ctas`, none of fewer than
+// `least` tiles.
+int pieces_for(long long units, long long ctas, long long tiles, int least) {
   const long long want = ctas / std::max(1LL, units);
-  return (int)std::max(1LL, std::min(std::min(want, (tiles + 3) / 4), 64LL));
+  return (int)std::max(1LL, std::min(std::min(want, (tiles + least - 1) / least), 64LL));
 }
 
 constexpr int kRowsCtas = 2 * kSMs;  // of the few-rows kernel: two per SM
@@ -355,8 +422,8 @@ constexpr long long kPrefixTiles = 4 * kRowsCtas;
 
 // Which kernel does which part.
 struct PrefixPlan {
-  int rg;                  // rows of a CUDA-core tile
-  int simt1, simt2;        // its row tiles: packed (prefix), of a request (own keys); 0: not its part
+  int rg1, rg2;            // rows of a CUDA-core tile: packed (prefix), of a request (own keys)
+  int simt1, simt2;        // such tiles; 0: not its part
   int tc1, tc2;            // 256-row tiles on the tensor cores, the same way
   bool fused, direct;      // request tiles take the prefix too; one piece in all, no merge
   int mt, groups;          // few-rows kernel: 16-row tiles (0: not used), row groups of the prefix
@@ -372,8 +439,7 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
   const int G = Hq / Hk;
   const long long rows = (long long)T * G, rows_q = (long long)max_q * G;
   const long long keys2 = (long long)table_ld * page;
-  w.rg = rows_q <= 16 ? 16 : 64;
-  auto tiles = [](long long n, int of) { return (int)((n + of - 1) / of); };
+  auto tiles = [](long long n, int of) { return (int)((n + of - 1) / of); };  // of a length
   auto mt_of = [](long long n) { return n <= 16 ? 1 : n <= 32 ? 2 : 4; };
   if (dt == BSA_BF16 && rows_q > kRowsMax) {
     // A request with more than 64 rows: 128-row tiles on the tensor cores.  Requests that fill half
@@ -397,15 +463,21 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
     w.own_rows = (int)rows_q;
     w.items = ((long long)w.groups + B) * Hk;
   } else {
-    w.simt1 = prefix_len ? tiles(rows, w.rg) : 0;
-    w.simt2 = keys2 ? tiles(rows_q, w.rg) : 0;
+    w.rg2 = rows_q <= 16 ? 16 : 64;
+    w.rg1 = w.rg2 == 64 || rows > 32 ? 64 : rows > 16 ? 32 : 16;
+    w.simt1 = prefix_len ? tiles(rows, w.rg1) : 0;
+    w.simt2 = keys2 ? tiles(rows_q, w.rg2) : 0;
   }
-  if (w.tc1) w.ns1 = pieces_for((long long)w.tc1 * Hk, kSMs, (prefix_len + 127) / 128);
-  if (w.simt1) w.ns1 = pieces_for((long long)w.simt1 * Hk, 2 * kSMs, (prefix_len + 63) / 64);
+  if (w.tc1) w.ns1 = pieces_for((long long)w.tc1 * Hk, kSMs, (prefix_len + 127) / 128, 4);
+  // Two CTAs per SM: half for the prefix, unless the own keys fill the GPU by themselves.
+  if (w.simt1)
+    w.ns1 = pieces_for((long long)w.simt1 * Hk,
+                       (long long)w.simt2 * B * Hk > 2 * kSMs ? 2 * kSMs : kSMs,
+                       tiles(prefix_len, 4096 / d), 2);
   if (w.tc2)
     w.ns2 = pieces_for((rows + 255) / 256 * Hk, kSMs,
-                       (keys2 + (w.fused ? prefix_len : 0) + 127) / 128);
-  if (w.simt2) w.ns2 = pieces_for((long long)w.simt2 * B * Hk, 2 * kSMs, (keys2 + 63) / 64);
+                       (keys2 + (w.fused ? prefix_len : 0) + 127) / 128, 4);
+  if (w.simt2) w.ns2 = pieces_for((long long)w.simt2 * B * Hk, kSMs, tiles(keys2, 4096 / d), 2);
   w.direct = w.tc2 && !w.tc1 && w.ns2 == 1;
   const long long all = w.direct ? 0 : (long long)T * Hq * (w.ns1 + w.ns2);
   w.ml_bytes = align_up((size_t)all * sizeof(float2), 256);
@@ -420,16 +492,16 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
   return w;
 }
 
-template <typename T, int D, int RG>
+template <int D, int RG1, int RG2>
 bsa_status launch_simt(const PrefixParams& p, const PrefixPlan& w, cudaStream_t st) {
   const long long units1 = (long long)w.simt1 * p.Hk * p.ns1;
   const long long units2 = (long long)p.B * w.simt2 * p.Hk * p.ns2;
   if (units1 + units2 > INT_MAX) return BSA_ERR_UNSUPPORTED;
   if (units1 + units2 == 0) return BSA_OK;
-  const int smem = SimtSmem<D, RG>::kTotal;
+  const int smem = std::max(SimtSmem<D, RG1>::kTotal, SimtSmem<D, RG2>::kTotal);
   static std::atomic<unsigned long long> done{0};
-  if (!allow_smem(prefix_simt_kernel<T, D, RG>, smem, done) ||
-      !launch_pdl(prefix_simt_kernel<T, D, RG>, (int)(units1 + units2), kPsThreads, smem, st, p,
+  if (!allow_smem(prefix_simt_kernel<D, RG1, RG2>, smem, done) ||
+      !launch_pdl(prefix_simt_kernel<D, RG1, RG2>, (int)(units1 + units2), kPsThreads, smem, st, p,
                   SimtGrid{(int)units1, w.simt2}))
     return BSA_ERR_CUDA;
   return BSA_OK;
@@ -437,19 +509,18 @@ bsa_status launch_simt(const PrefixParams& p, const PrefixPlan& w, cudaStream_t 
 
 template <typename T, int D>
 bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status, cudaStream_t st) {
+  bsa_status rc = BSA_OK;
   if constexpr (sizeof(T) == 2) {
-    const bsa_status rc = prefix_attn_tc(p, D, w.tc1, w.tc2, w.fused, w.direct, status, st);
+    rc = prefix_attn_tc(p, D, w.tc1, w.tc2, w.fused, w.direct, status, st);
     if (rc != BSA_OK || w.direct) return rc;
-    if (w.mt) {
-      const bsa_status rr = prefix_attn_rows(p, D, w.mt, w.groups, w.tc1 > 0, status, st);
-      if (rr != BSA_OK) return rr;
-    }
+    if (w.mt) rc = prefix_attn_rows(p, D, w.mt, w.groups, w.tc1 > 0, status, st);
+  } else {
+    rc = w.rg2 == 64   ? launch_simt<D, 64, 64>(p, w, st)
+         : w.rg1 == 64 ? launch_simt<D, 64, 16>(p, w, st)
+         : w.rg1 == 32 ? launch_simt<D, 32, 16>(p, w, st)
+                       : launch_simt<D, 16, 16>(p, w, st);
   }
-  if (w.simt1 || w.simt2) {
-    const bsa_status rc =
-        w.rg == 16 ? launch_simt<T, D, 16>(p, w, st) : launch_simt<T, D, 64>(p, w, st);
-    if (rc != BSA_OK) return rc;
-  }
+  if (rc != BSA_OK) return rc;
   const long long rows = (long long)p.T * p.Hq;
   return launch_pdl(prefix_merge_kernel<T, D>, (int)((rows + 7) / 8), 256, 0, st, p)
              ? BSA_OK

@@ -298,113 +298,15 @@ __global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixPar
   }
 }
 
-// Joins the pieces of a row: a warp per row, d / 32 columns per lane.
+// Joins the pieces of a row, a warp per row.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) prefix_merge_kernel(const PrefixParams p) {
-  constexpr int C = D / 32;
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long rows = (long long)p.T * p.Hq;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const int t = (int)(row / p.Hq), hq = (int)(row - (long long)t * p.Hq);
-  if (t >= pa_tokens(p)) return;
-  int b = t;
-  if (p.cu_q) {
-    // the request of the token: how many requests end at or before it
-    b = 0;
-    for (int i = 0; i < p.B; i += 32) {
-      const bool before = i + lane < p.B && p.cu_q[i + lane + 1] <= t;
-      b += __popc(__ballot_sync(0xffffffffu, before));
-    }
-    // tokens beyond max_q of their request were not attended
-    if (b >= p.B || t - p.cu_q[b] >= p.max_q) return;
-  }
-  // the row's pieces: dense ones, then up to two runs of item slots (first row, rows from one to
-  // the next, how many)
-  long long first0 = 0, first1 = 0;
-  int count0 = 0, count1 = 0;
-  if (p.item_ctas) {
-    const int h = hq >> p.g_shift, g = hq & (p.G - 1);
-    auto pieces = [&](int item, int r, long long& first, int& count) {
-      const int2 c = p.item_cta[item];  // cut: a run that stopped early has not written it
-      const int c0 = min(max(c.x, 0), p.item_ctas - 1), c1 = min(max(c.y, c0), p.item_ctas - 1);
-      first = pa_item_row(p, item, c0) + r;
-      count = c1 - c0 + 1;
-    };
-    if (p.prefix_items) {
-      const int groups = p.prefix_items / p.Hk, r = (t << p.g_shift) + g;
-      const int at = r / p.prefix_rows;  // its group
-      pieces(h * groups + at, r - at * p.prefix_rows, first0, count0);
-    }
-    const PaRequest r = pa_request(p, b);
-    if (pa_own_keys(p, r) > 0)
-      pieces(p.prefix_items + b * p.Hk + h, ((t - r.t0) << p.g_shift) + g, first1, count1);
-  }
-  const int ns = p.ns1 + p.ns2, n = ns + count0 + count1;
-  auto piece = [&](int s, const float2*& ml, const float*& o) {
-    if (s < ns) {
-      const long long i = s * rows + row;
-      ml = p.part_ml + i;
-      o = p.part_o + i * D;
-    } else {
-      const int e = s - ns;
-      const long long i = e < count0 ? first0 + (long long)e * p.prefix_rows
-                                     : first1 + (long long)(e - count0) * p.own_rows;
-      ml = p.item_ml + i;
-      o = p.item_o + i * D;
-    }
-  };
-  // running maximum and sum over the pieces, kAhead of them loaded together
-  constexpr int kAhead = 8;
-  float top = -INFINITY, l = 0.f, acc[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) acc[c] = 0.f;
-  for (int s0 = 0; s0 < n; s0 += kAhead) {
-    float2 ml[kAhead];
-    float x[kAhead][C];
-#pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
-      ml[e] = make_float2(-INFINITY, 0.f);
-      if (s0 + e < n) {
-        const float2* mp;
-        const float* op;
-        piece(s0 + e, mp, op);
-        ml[e] = *mp;
-        load_vec<float, C>(op + lane * C, x[e]);
-      }
-    }
-    float m = top;
-#pragma unroll
-    for (int e = 0; e < kAhead; ++e) m = fmaxf(m, ml[e].x);
-    const float keep = m == -INFINITY ? 1.f : exp2f(top - m);
-    top = m;
-    l *= keep;
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] *= keep;
-#pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
-      if (ml[e].y == 0.f) continue;  // no key in the piece: its o was not written
-      const float w = exp2f(ml[e].x - top);
-      l += ml[e].y * w;
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] += x[e][c] * w;
-    }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;  // no key at all: o = 0
-  T* op = static_cast<T*>(p.o) + row * D + lane * C;
-  if constexpr (sizeof(T) == 2) {
-    __nv_bfloat162 w[C / 2];
-#pragma unroll
-    for (int c = 0; c < C; c += 2) w[c / 2] = __floats2bfloat162_rn(acc[c] * inv, acc[c + 1] * inv);
-    if constexpr (C == 4) *reinterpret_cast<uint2*>(op) = *reinterpret_cast<uint2*>(w);
-    else *reinterpret_cast<uint32_t*>(op) = *reinterpret_cast<uint32_t*>(w);
-  } else {
-#pragma unroll
-    for (int c = 0; c < C; c += 2)
-      *reinterpret_cast<float2*>(op + c) = make_float2(acc[c] * inv, acc[c + 1] * inv);
-  }
-  if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kPaLn2;
+  if (row >= (long long)p.T * p.Hq) return;
+  const int t = (int)(row / p.Hq);
+  if (t < pa_tokens(p))
+    pa_join_row<T, D>(p, t, (int)(row - (long long)t * p.Hq), threadIdx.x & 31);
 }
 
 // How the keys are cut: enough pieces that `units` CTAs a piece fill `ctas`, none of fewer than
@@ -416,6 +318,8 @@ int pieces_for(long long units, long long ctas, long long tiles, int least) {
 
 constexpr int kRowsCtas = 2 * kSMs;  // of the few-rows kernel: two per SM
 constexpr int kRowsMax = 64;         // its rows
+constexpr int kClusterCtas = 16;     // of a kv head in a small call
+constexpr long long kClusterTiles = 4 * kClusterCtas;  // key tiles of a kv head up to which one is small
 // Key tiles of 32 KB (over all heads and row groups) up to which the few-rows kernel takes the prefix of
 // more rows: four a CTA.
 constexpr long long kPrefixTiles = 4 * kRowsCtas;
@@ -426,8 +330,9 @@ struct PrefixPlan {
   int simt1, simt2;        // such tiles; 0: not its part
   int tc1, tc2;            // 256-row tiles on the tensor cores, the same way
   bool fused, direct;      // request tiles take the prefix too; one piece in all, no merge
+  bool cluster;            // few-rows kernel as one cluster per kv head, which joins the pieces itself
   int mt, groups;          // few-rows kernel: 16-row tiles (0: not used), row groups of the prefix
-  int ns1, ns2, prefix_rows, own_rows;
+  int ns1, ns2, prefix_rows, own_rows, item_ctas;
   long long items;
   size_t ml_bytes, o_bytes, cta_bytes, item_ml_bytes, item_o_bytes;
   size_t bytes() const { return ml_bytes + o_bytes + cta_bytes + item_ml_bytes + item_o_bytes; }
@@ -462,6 +367,11 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
     w.prefix_rows = 16 * w.mt;
     w.own_rows = (int)rows_q;
     w.items = ((long long)w.groups + B) * Hk;
+    // A small call is one launch: a cluster per kv head (4 requests behind 1000 tokens: 11.5 us as two).
+    // With fewer CTAs than the GPU holds it loses that again once each has several tiles.
+    w.cluster = !w.tc1 && (long long)w.groups * tiles(prefix_len, 8192 / d) +
+                                  (long long)B * tiles(keys2, 8192 / d) <= kClusterTiles;
+    w.item_ctas = w.cluster ? kClusterCtas : kRowsCtas;
   } else {
     w.rg2 = rows_q <= 16 ? 16 : 64;
     w.rg1 = w.rg2 == 64 || rows > 32 ? 64 : rows > 16 ? 32 : 16;
@@ -483,8 +393,9 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
   w.ml_bytes = align_up((size_t)all * sizeof(float2), 256);
   w.o_bytes = align_up((size_t)all * d * sizeof(float), 256);
   if (w.mt) {
-    const size_t n = (w.groups ? ((size_t)w.groups * Hk + kRowsCtas) * w.prefix_rows : 0) +
-                     ((size_t)B * Hk + kRowsCtas) * w.own_rows;
+    const size_t ctas = (size_t)w.item_ctas * (w.cluster ? Hk : 1);
+    const size_t n = (w.groups ? ((size_t)w.groups * Hk + ctas) * w.prefix_rows : 0) +
+                     ((size_t)B * Hk + ctas) * w.own_rows;
     w.cta_bytes = align_up((size_t)w.items * sizeof(int2), 256);
     w.item_ml_bytes = align_up(n * sizeof(float2), 256);
     w.item_o_bytes = n * d * sizeof(float);
@@ -501,7 +412,8 @@ bsa_status launch_simt(const PrefixParams& p, const PrefixPlan& w, cudaStream_t 
   const int smem = std::max(SimtSmem<D, RG1>::kTotal, SimtSmem<D, RG2>::kTotal);
   static std::atomic<unsigned long long> done{0};
   if (!allow_smem(prefix_simt_kernel<D, RG1, RG2>, smem, done) ||
-      !launch_pdl(prefix_simt_kernel<D, RG1, RG2>, (int)(units1 + units2), kPsThreads, smem, st, p,
+      !launch_pdl(prefix_simt_kernel<D, RG1, RG2>, (int)(units1 + units2), 1, kPsThreads, smem, st,
+                  p,
                   SimtGrid{(int)units1, w.simt2}))
     return BSA_ERR_CUDA;
   return BSA_OK;
@@ -513,7 +425,8 @@ bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status,
   if constexpr (sizeof(T) == 2) {
     rc = prefix_attn_tc(p, D, w.tc1, w.tc2, w.fused, w.direct, status, st);
     if (rc != BSA_OK || w.direct) return rc;
-    if (w.mt) rc = prefix_attn_rows(p, D, w.mt, w.groups, w.tc1 > 0, status, st);
+    if (w.mt) rc = prefix_attn_rows(p, D, w.mt, w.tc1 > 0, status, st);
+    if (rc != BSA_OK || w.cluster) return rc;
   } else {
     rc = w.rg2 == 64   ? launch_simt<D, 64, 64>(p, w, st)
          : w.rg1 == 64 ? launch_simt<D, 64, 16>(p, w, st)
@@ -522,7 +435,7 @@ bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status,
   }
   if (rc != BSA_OK) return rc;
   const long long rows = (long long)p.T * p.Hq;
-  return launch_pdl(prefix_merge_kernel<T, D>, (int)((rows + 7) / 8), 256, 0, st, p)
+  return launch_pdl(prefix_merge_kernel<T, D>, (int)((rows + 7) / 8), 1, 256, 0, st, p)
              ? BSA_OK
              : BSA_ERR_CUDA;
 }
@@ -600,8 +513,9 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
   p.ns1 = w.ns1; p.ns2 = w.ns2;
   p.prefix_rows = w.prefix_rows;
   p.own_rows = w.own_rows;
-  p.item_ctas = w.mt ? kRowsCtas : 0;
-  p.prefix_items = w.groups * Hk;
+  p.item_ctas = w.item_ctas;
+  p.groups = w.groups;
+  p.cluster = w.cluster;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dt == BSA_BF16)
     return d == 64 ? launch_parts<__nv_bfloat16, 64>(p, w, status, st)

@@ -30,13 +30,16 @@ struct PrefixParams {
   float* part_o;
   float2* part_ml;
   int ns1, ns2;
-  // Pieces of prefix_attn_rows: items are the prefix_items = Hk * groups of packed rows x prefix, then
-  // request * Hk + kv head; item_cta[item] = first and last CTA that worked on it; the piece of CTA
-  // c is slot item + c, of prefix_rows rows for a prefix item and own_rows for another (pa_item_row).
-  int2* item_cta;
-  float* item_o;    // [row][d]
-  float2* item_ml;  // [row]
-  int prefix_rows, own_rows, item_ctas, prefix_items;  // item_ctas = 0: no items
+  // Pieces of prefix_attn_rows: an item is a kv head and a group of packed rows (prefix) or a request
+  // (own keys); *_cta[item] = first and last CTA that worked on it, and CTA c's piece of it is a run
+  // of prefix_rows / own_rows rows of item_o [row][d] and item_ml [row] (pa_piece_row).
+  int groups;       // row groups of the prefix, 0: the prefix is not among the items
+  int2* item_cta;   // [Hk * groups] prefix items, then [B * Hk] own ones
+  float* item_o;
+  float2* item_ml;
+  int prefix_rows, own_rows;
+  int item_ctas;  // CTAs that share the items, 0: no items
+  int cluster;    // they are one cluster per kv head, which also joins its pieces
 };
 
 // Request b: its first new token, how many it has, its own tokens.  Values that would reach
@@ -60,15 +63,131 @@ __device__ __forceinline__ PaRequest pa_request(const PrefixParams& p, int b) {
 __device__ __forceinline__ int pa_own_keys(const PrefixParams& p, const PaRequest& r) {
   return r.nq > 0 ? max(0, r.len - r.nq + min(r.nq, p.max_q)) : 0;
 }
-// First row of the piece that CTA c has of an item.
-__device__ __forceinline__ long long pa_item_row(const PrefixParams& p, int item, int c) {
-  if (item < p.prefix_items) return (long long)(item + c) * p.prefix_rows;
-  return (long long)(p.prefix_items ? p.prefix_items + p.item_ctas : 0) * p.prefix_rows +
-         (long long)(item - p.prefix_items + c) * p.own_rows;
+__device__ __forceinline__ int2* pa_item_cta(const PrefixParams& p, bool prefix, int h, int i) {
+  return p.item_cta + (prefix ? (size_t)h * p.groups + i
+                              : (size_t)p.Hk * p.groups + (size_t)i * p.Hk + h);
+}
+// First row of CTA c's piece of an item: kv head h, group or request i.  CTAs and items both only grow
+// along the order in which the items' tiles are dealt out, so item + CTA is a place of its own; with a
+// cluster per head, the order is within the head.
+__device__ __forceinline__ long long pa_piece_row(const PrefixParams& p, bool prefix, int h, int i,
+                                                  int c) {
+  const long long before =  // pieces of the prefix
+      p.groups == 0 ? 0
+      : p.cluster   ? (long long)p.Hk * (p.groups + p.item_ctas)
+                    : (long long)p.Hk * p.groups + p.item_ctas;
+  if (prefix)
+    return (p.cluster ? (long long)h * (p.groups + p.item_ctas) + i : (long long)h * p.groups + i) *
+               p.prefix_rows + (long long)c * p.prefix_rows;
+  return before * p.prefix_rows +
+         (p.cluster ? (long long)h * (p.B + p.item_ctas) + i : (long long)i * p.Hk + h) *
+             p.own_rows + (long long)c * p.own_rows;
 }
 // New tokens in all: rows at or after this are left as they were.
 __device__ __forceinline__ int pa_tokens(const PrefixParams& p) {
   return p.cu_q ? min(max(p.cu_q[p.B], 0), p.T) : p.B;
+}
+
+// Joins the pieces of row (token t, query head hq) and writes o and lse: a warp, d / 32 columns per
+// lane.  t is a token of a request.
+template <typename T, int D>
+__device__ __forceinline__ void pa_join_row(const PrefixParams& p, int t, int hq, int lane) {
+  constexpr int C = D / 32;
+  const long long rows = (long long)p.T * p.Hq, row = (long long)t * p.Hq + hq;
+  int b = t;
+  if (p.cu_q) {
+    // the request of the token: how many requests end at or before it
+    b = 0;
+    for (int i = 0; i < p.B; i += 32) {
+      const bool before = i + lane < p.B && p.cu_q[i + lane + 1] <= t;
+      b += __popc(__ballot_sync(0xffffffffu, before));
+    }
+    // tokens before the first request and beyond max_q of their own were not attended
+    if (b >= p.B || t < p.cu_q[b] || t - p.cu_q[b] >= p.max_q) return;
+  }
+  // the row's pieces: dense ones, then up to two runs of item slots (first row, rows from one to
+  // the next, how many)
+  long long first0 = 0, first1 = 0;
+  int count0 = 0, count1 = 0;
+  if (p.item_ctas) {
+    const int h = hq >> p.g_shift, g = hq & (p.G - 1);
+    auto pieces = [&](bool prefix, int i, int r, long long& first, int& count) {
+      const int2 c = *pa_item_cta(p, prefix, h, i);  // cut: a run that stopped early has not set it
+      const int c0 = min(max(c.x, 0), p.item_ctas - 1), c1 = min(max(c.y, c0), p.item_ctas - 1);
+      first = pa_piece_row(p, prefix, h, i, c0) + r;
+      count = c1 - c0 + 1;
+    };
+    if (p.groups) {
+      const int r = (t << p.g_shift) + g, i = r / p.prefix_rows;  // its group
+      pieces(true, i, r - i * p.prefix_rows, first0, count0);
+    }
+    const PaRequest r = pa_request(p, b);
+    if (pa_own_keys(p, r) > 0) pieces(false, b, ((t - r.t0) << p.g_shift) + g, first1, count1);
+  }
+  const int ns = p.ns1 + p.ns2, n = ns + count0 + count1;
+  auto piece = [&](int s, const float2*& ml, const float*& o) {
+    if (s < ns) {
+      const long long i = s * rows + row;
+      ml = p.part_ml + i;
+      o = p.part_o + i * D;
+    } else {
+      const int e = s - ns;
+      const long long i = e < count0 ? first0 + (long long)e * p.prefix_rows
+                                     : first1 + (long long)(e - count0) * p.own_rows;
+      ml = p.item_ml + i;
+      o = p.item_o + i * D;
+    }
+  };
+  // running maximum and sum over the pieces, kAhead of them loaded together
+  constexpr int kAhead = 8;
+  float top = -INFINITY, l = 0.f, acc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] = 0.f;
+  for (int s0 = 0; s0 < n; s0 += kAhead) {
+    float2 ml[kAhead];
+    float x[kAhead][C];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      ml[e] = make_float2(-INFINITY, 0.f);
+      if (s0 + e < n) {
+        const float2* mp;
+        const float* op;
+        piece(s0 + e, mp, op);
+        ml[e] = *mp;
+        load_vec<float, C>(op + lane * C, x[e]);
+      }
+    }
+    float m = top;
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) m = fmaxf(m, ml[e].x);
+    const float keep = m == -INFINITY ? 1.f : exp2f(top - m);
+    top = m;
+    l *= keep;
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] *= keep;
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      if (ml[e].y == 0.f) continue;  // no key in the piece: its o was not written
+      const float w = exp2f(ml[e].x - top);
+      l += ml[e].y * w;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] += x[e][c] * w;
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // no key at all: o = 0
+  T* op = static_cast<T*>(p.o) + row * D + lane * C;
+  if constexpr (sizeof(T) == 2) {
+    __nv_bfloat162 w[C / 2];
+#pragma unroll
+    for (int c = 0; c < C; c += 2) w[c / 2] = __floats2bfloat162_rn(acc[c] * inv, acc[c + 1] * inv);
+    if constexpr (C == 4) *reinterpret_cast<uint2*>(op) = *reinterpret_cast<uint2*>(w);
+    else *reinterpret_cast<uint32_t*>(op) = *reinterpret_cast<uint32_t*>(w);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; c += 2)
+      *reinterpret_cast<float2*>(op + c) = make_float2(acc[c] * inv, acc[c + 1] * inv);
+  }
+  if (lane == 0 && p.lse) p.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kPaLn2;
 }
 
 // The call's kernels are launched as programmatic dependents, so that one's launch and prologue run
@@ -79,10 +198,10 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 template <typename... Args>
-bool launch_pdl(void (*kern)(Args...), int grid, int threads, int smem, cudaStream_t st,
-                const Args&... args) {
+bool launch_pdl(void (*kern)(Args...), int grid, int cluster, int threads, int smem,
+                cudaStream_t st, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3((unsigned)grid);
@@ -91,20 +210,30 @@ bool launch_pdl(void (*kern)(Args...), int grid, int threads, int smem, cudaStre
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
   if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return true;
   (void)cudaGetLastError();
   return false;
 }
 
-// Dynamic shared memory above 48 KB, asked for once per device (`done`: one bit each).
+// Dynamic shared memory above 48 KB and clusters above 8 CTAs, asked for once per device (`done`: one
+// bit each).
 template <typename Kern>
-bool allow_smem(Kern kern, int bytes, std::atomic<unsigned long long>& done) {
+bool allow_smem(Kern kern, int bytes, std::atomic<unsigned long long>& done,
+                bool large_cluster = false) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (bit && (done.load(std::memory_order_relaxed) & bit)) return true;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-      cudaSuccess) {
+          cudaSuccess ||
+      (large_cluster && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                             1) != cudaSuccess)) {
     (void)cudaGetLastError();
     return false;
   }
@@ -130,7 +259,7 @@ bsa_status prefix_attn_tc(const PrefixParams& p, int d, int tiles1, int tiles2, 
                           bool direct, int* status, cudaStream_t st);
 
 // prefix_attn_rows.cu
-bsa_status prefix_attn_rows(const PrefixParams& p, int d, int mt, int groups, bool after_tc,
-                            int* status, cudaStream_t st);
+bsa_status prefix_attn_rows(const PrefixParams& p, int d, int mt, bool after_tc, int* status,
+                            cudaStream_t st);
 
 }  // namespace bsa

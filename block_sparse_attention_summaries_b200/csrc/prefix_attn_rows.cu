@@ -8,7 +8,8 @@
 // CTAs per SM), whatever the requests' lengths: a CTA's producer warp walks its run without stopping
 // at item borders, so the ring of tiles stays full while the consumers change rows.  An item is then
 // cut into at most the pieces that its CTAs saw; piece (item, CTA) is stored at slot item + CTA,
-// unique because both only grow along the run, and the merge kernel joins an item's slots.
+// unique because both only grow along the run, and the merge kernel joins an item's slots.  In a small
+// call a cluster of CTAs does this per kv head and joins the pieces itself behind a cluster barrier.
 //   warps 0-3: per tile, S of 16 or 32 keys each for MT tiles of 16 rows (mma.sync m16n8k16: an M = 128
 //              tcgen05 tile would be padding for half its rows or more, and HBM bounds the rate far
 //              below either); the row maxima meet in shared memory, each warp exponentiates its
@@ -20,6 +21,8 @@
 //              wait for memory (items of one tile took 5 us each before, 64 x 64 tokens x 8 heads
 //              15.8 us in all, now 11.2 us)
 // V rows without a key are masked to zero in the registers that feed the products.
+#include <cooperative_groups.h>
+
 #include "prefix_attn.cuh"
 
 namespace bsa {
@@ -49,7 +52,8 @@ struct RowsSmem {
 
 // What the producer tells the consumers about a tile.
 struct TileInfo {
-  int item, nrows, first_pos;
+  int prefix, h, i;  // item: of the prefix or not, kv head, group or request
+  int nrows, first_pos;
   int j0, n;      // its first key; keys of the item
   uint32_t have;  // boxes on pages of the pool | first tile of the run's piece << 16 | last << 17
                   // | query buffer << 18
@@ -58,7 +62,6 @@ struct TileInfo {
 constexpr uint32_t kFirst = 1u << 16, kLast = 1u << 17;
 
 struct RowsGrid {
-  int groups;        // row groups of the prefix, 0: the prefix is not this kernel's part
   int box_shift;     // rows of a box
   int after_tc;      // a kernel of the same call runs before: its results are not read here
   int* status;
@@ -147,21 +150,23 @@ __global__ void __launch_bounds__(kRThreads, 2)
     }
   }
   __syncthreads();
-  const int ptiles = g.groups ? (p.prefix_len + kRKeys - 1) / kRKeys : 0;
-  const int pitems = p.prefix_items;
-  const long long total = (long long)pitems * ptiles + (long long)p.Hk * s_sum[kRThreads - 1];
+  const int ptiles = p.groups ? (p.prefix_len + kRKeys - 1) / kRKeys : 0;
+  // the heads whose tiles are dealt out: all, or the cluster's
+  const int heads = p.cluster ? 1 : p.Hk, head0 = p.cluster ? blockIdx.x / p.item_ctas : 0;
+  const int me = p.cluster ? blockIdx.x % p.item_ctas : blockIdx.x;
+  const int pitems = heads * p.groups;
+  const long long total = (long long)pitems * ptiles + (long long)heads * s_sum[kRThreads - 1];
   // no CTA within a run of pieces may be without one: at most as many CTAs work as there are tiles
-  const long long ctas = min((long long)gridDim.x, total);
-  if (blockIdx.x >= ctas) {
-    if (g.after_tc) pdl_wait();  // this kernel is not complete before the one before it
-    return;
-  }
-  const long long f0 = total * blockIdx.x / ctas, f1 = total * (blockIdx.x + 1) / ctas;
-  const int count = (int)(f1 - f0);
+  const long long ctas = min((long long)p.item_ctas, total);
+  const long long f0 = me < ctas ? total * me / ctas : 0;
+  const int count = me < ctas ? (int)(total * (me + 1) / ctas - f0) : 0;
 
-  if (warp == 4) {
+  if (count == 0) {
+    // nothing to attend
+  } else if (warp == 4) {
     // ------------------------------------------------------------------------- producer
-    // where the run is: request (-1: the prefix), kv head (prefix: item), tile of the item
+    // where the run is: request (-1: the prefix), head of the run's (prefix: head * groups + group),
+    // tile of the item
     struct Place {
       int b, h, tile, tiles, n, t0, nrows, first_pos;
     } c;
@@ -184,10 +189,9 @@ __global__ void __launch_bounds__(kRThreads, 2)
       x.nrows = min(r.nq, p.max_q) << p.g_shift;
       x.first_pos = r.len - r.nq;
     };
-    // prefix item: kv head h / groups, packed rows from (h % groups) * 16 MT
-    const int prefix_rows = g.groups ? pa_tokens(p) << p.g_shift : 0;
+    const int prefix_rows = p.groups ? pa_tokens(p) << p.g_shift : 0;
     auto enter_prefix = [&](Place& x, int h) {
-      const int r0 = h % g.groups * 16 * MT;
+      const int r0 = h % p.groups * 16 * MT;
       x.b = -1;
       x.h = h;
       x.tiles = ptiles;
@@ -201,14 +205,14 @@ __global__ void __launch_bounds__(kRThreads, 2)
     } else {
       const long long f = f0 - (long long)pitems * ptiles;
       int th = 0;
-      while ((long long)p.Hk * s_sum[th] <= f) ++th;
+      while ((long long)heads * s_sum[th] <= f) ++th;
       long long before = th ? s_sum[th - 1] : 0;
       enter(c, th * per);
-      while ((long long)p.Hk * (before + c.tiles) <= f) {
+      while ((long long)heads * (before + c.tiles) <= f) {
         before += c.tiles;
         enter(c, c.b + 1);
       }
-      const int rest = (int)(f - (long long)p.Hk * before);
+      const int rest = (int)(f - (long long)heads * before);
       c.h = rest / c.tiles;
       c.tile = rest - c.h * c.tiles;
     }
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kRThreads, 2)
         ++nx.h;
         if (nx.b < 0 && nx.h < pitems) {
           enter_prefix(nx, nx.h);
-        } else if (nx.b < 0 || nx.h == p.Hk) {
+        } else if (nx.b < 0 || nx.h == heads) {
           nx.h = 0;
           do {
             ok = nx.b + 1 < p.B;  // holds unless the lengths change under the call
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(kRThreads, 2)
       const int next_id = done + 1 < count ? page_at(nx) : -1;
       const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
       const bool last = ends || done + 1 == count;
-      const int kh = c.b < 0 ? c.h / g.groups : c.h;
+      const int kh = head0 + (c.b < 0 ? c.h / p.groups : c.h);
       const int qb = piece % L::kQBufs;
       // a page of 128 holds two boxes
       const int j = c.tile * kRKeys + (lane << g.box_shift);
@@ -265,15 +269,17 @@ __global__ void __launch_bounds__(kRThreads, 2)
         if (lane == 0) {
           if (kv == 0) {
             TileInfo t;
-            t.item = c.b < 0 ? c.h : pitems + c.b * p.Hk + c.h;
+            t.prefix = c.b < 0;
+            t.h = kh;
+            t.i = c.b < 0 ? c.h % p.groups : c.b;
             t.nrows = c.nrows;
             t.first_pos = c.first_pos;
             t.j0 = c.tile * kRKeys;
             t.n = c.n;
             t.have = have | (first ? kFirst : 0u) | (last ? kLast : 0u) | (uint32_t)qb << 18;
             s_info[done % (kInfos + 1)] = t;
-            if (c.tile == 0) p.item_cta[t.item].x = blockIdx.x;
-            if (ends) p.item_cta[t.item].y = blockIdx.x;
+            if (c.tile == 0) pa_item_cta(p, c.b < 0, kh, t.i)->x = me;
+            if (ends) pa_item_cta(p, c.b < 0, kh, t.i)->y = me;
           }
           mbar_arrive_expect_tx(&full[sl], (uint32_t)__popc(have) * box_bytes * (D / 64) +
                                                (queries ? (uint32_t)L::kQTile : 0u));
@@ -488,7 +494,7 @@ __global__ void __launch_bounds__(kRThreads, 2)
             if ((lane & 3) == 0) s_l[buf][warp][16 * mt + qr + 8 * a] = x;
           }
         bar_consumers();
-        const long long slot = pa_item_row(p, t.item, (int)blockIdx.x);
+        const long long slot = pa_piece_row(p, t.prefix, t.h, t.i, me);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -510,6 +516,13 @@ __global__ void __launch_bounds__(kRThreads, 2)
   __syncthreads();
   if (s_abort && tid == 0) report_timeout(g.status, 6);
   if (g.after_tc) pdl_wait();  // this kernel is not complete before the one before it
+  if (p.cluster) {
+    // the head's pieces are all written: join its rows here
+    cooperative_groups::this_cluster().sync();
+    const int n = pa_tokens(p) << p.g_shift;
+    for (int r = me * (kRThreads / 32) + warp; r < n; r += p.item_ctas * (kRThreads / 32))
+      pa_join_row<__nv_bfloat16, D>(p, r >> p.g_shift, (head0 << p.g_shift) + (r & (p.G - 1)), lane);
+  }
 }
 
 template <int D, int MT>
@@ -522,21 +535,20 @@ bsa_status launch_rows(const PrefixParams& p, const RowsGrid& g, cudaStream_t st
   const int smem = L::kTotal + 1024;  // + alignment slack
   static_assert(2 * (L::kTotal + 1024 + 4096 + 1024) <= 228 * 1024, "two CTAs per SM");
   static std::atomic<unsigned long long> done{0};
-  if (!allow_smem(prefix_rows_kernel<D, MT>, smem, done) ||
-      !launch_pdl(prefix_rows_kernel<D, MT>, p.item_ctas, kRThreads, smem, st, tmq, tmk, tmv, p,
-                  g))
+  if (!allow_smem(prefix_rows_kernel<D, MT>, smem, done, true) ||
+      !launch_pdl(prefix_rows_kernel<D, MT>, p.item_ctas * (p.cluster ? p.Hk : 1),
+                  p.cluster ? p.item_ctas : 1, kRThreads, smem, st, tmq, tmk, tmv, p, g))
     return BSA_ERR_CUDA;
   return BSA_OK;
 }
 
 }  // namespace
 
-// Own keys of every request, with up to 16 mt rows each, and the prefix for `groups` groups of as
-// many packed rows (0: not the prefix).
-bsa_status prefix_attn_rows(const PrefixParams& p, int d, int mt, int groups, bool after_tc,
-                            int* status, cudaStream_t st) {
+// Own keys of every request, with up to 16 mt rows each, and the prefix for p.groups groups of as
+// many packed rows.
+bsa_status prefix_attn_rows(const PrefixParams& p, int d, int mt, bool after_tc, int* status,
+                            cudaStream_t st) {
   RowsGrid g;
-  g.groups = groups;
   g.box_shift = std::min(p.page_shift, d == 64 ? 7 : 6);
   g.after_tc = after_tc;
   g.status = status;

@@ -617,7 +617,7 @@ bsa_status launch_tc(const PrefixParams& p, const TcGrid& g, int grid, cudaStrea
   const int smem = TcSmem<D>::kTotal + 1024;  // + alignment slack
   static std::atomic<unsigned long long> done{0};
   if (!allow_smem(prefix_tc_kernel<D>, smem, done) ||
-      !launch_pdl(prefix_tc_kernel<D>, grid, kXThreads, smem, st, tmq, tmk, tmv, p, g))
+      !launch_pdl(prefix_tc_kernel<D>, grid, 1, kXThreads, smem, st, tmq, tmk, tmv, p, g))
     return BSA_ERR_CUDA;
   return BSA_OK;
 }

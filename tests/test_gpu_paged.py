@@ -252,6 +252,32 @@ def test_tokens_beyond_max_q_are_left(dtype):
     assert (o[3 + 4:3 + 9] == 7).all() and (o[3:3 + 4] != 7).any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("nq", [[2, 1], [70, 3], [200, 1]])
+def test_tokens_before_the_first_request_are_left(dtype, nq):
+    """cu_q may start behind the first token, as a slice of a longer batch does."""
+    m = Batch(14, dtype, 8, 2, 64, 16, 90, nq, [300, 20], pad_tokens=5)
+    q = m.q.clone()
+    m.q[5:] = q[:-5]
+    m.cu = m.cu + 5
+    o = torch.full(m.q.shape, 7.0, device=DEV, dtype=dtype)
+    lse = torch.full(m.q.shape[:2], 7.0, device=DEV)
+    m.run(o=o, lse=lse)
+    assert (o[:5] == 7).all() and (lse[:5] == 7).all()
+    m.q = m.q[5:]
+    m.check(o[5:], lse[5:])
+
+
+@pytest.mark.parametrize("B,n,ld", [(1, 1, 1), (2, 17, 2), (9, 40, 3), (30, 64, 4), (60, 16, 1)])
+@pytest.mark.parametrize("heads,kv_heads,d", [(8, 8, 64), (32, 8, 128), (8, 1, 128)])
+def test_small_calls(B, n, ld, heads, kv_heads, d):
+    """Small enough for one launch, up to and past the border; again with the lengths grown."""
+    m = Batch(15, BF16, heads, kv_heads, d, 16, 100, [1] * B, [1 + (n + i) % n for i in range(B)],
+              decode=True, spare_ld=ld)
+    for _ in range(2):
+        m.check(*m.run())
+
+
 def test_repeats_bit_for_bit():
     m = Batch(11, BF16, 32, 8, 128, 64, 5000, [1] * 40, list(range(1, 41)), decode=True)
     a, la = m.run()

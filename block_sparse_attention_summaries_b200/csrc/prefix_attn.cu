@@ -11,10 +11,13 @@
 // keys when there are too few tiles to fill the GPU; prefix_merge_kernel joins a row's pieces.
 //
 // prefix_simt_kernel: float32, CUDA cores (its tensor-core formats would round q, k and the weights).
-// A CTA of 256 threads takes RG rows (of one kv head, row = token * G + head of the group) and a
+// A CTA of 128 threads takes RG rows (of one kv head, row = token * G + head of the group) and a
 // piece of the keys in tiles of 64 (d = 64) or 32: S = Q K^T in registers from shared memory, online
-// softmax with the running maximum and sum of each row in registers of the 16 threads that share
-// it, P through shared memory, O += P V in registers.  The next tile is copied (cp.async) while one is
+// softmax with the running maximum of each row in registers of the 8 threads that share it, P through
+// shared memory, O += P V in registers.  A warp is 4 x 8 threads of 4 rows and 8 keys each (RG = 64,
+// d = 64), so that its reads of Q and of K are one shared-memory wavefront each: with 2 x 16 threads of
+// 4 x 4 the wavefronts (79 % of their peak) held the FMAs at 50 % (159 requests behind 46K keys: 1.10
+// ms).  The next tile is copied (cp.async) while one is
 // worked on, its page ids read a tile earlier still: with loads in line a tile took 5 us, the time of
 // two dependent trips to memory.
 #include "prefix_attn.cuh"
@@ -22,7 +25,7 @@
 namespace bsa {
 namespace {
 
-constexpr int kPsThreads = 256;
+constexpr int kPsThreads = 128;
 
 template <int D, int RG>
 struct SimtSmem {
@@ -60,12 +63,12 @@ template <int D, int RG>
 __device__ __forceinline__ void simt_unit(const PrefixParams& p, const SimtUnit& un, float* smf) {
   using L = SimtSmem<D, RG>;
   constexpr int TM = RG / 16;           // rows of a thread
-  constexpr int NE = L::kKeys / 16;     // keys of a thread's scores
-  constexpr int DC = D / 64;            // float4 columns of a thread
+  constexpr int NE = L::kKeys / 8;      // keys of a thread's scores
+  constexpr int DC = D / 32;            // float4 columns of a thread
   constexpr int RPP = kPsThreads / (D / 4);  // key rows copied at a time
   constexpr int NR = L::kKeys / RPP;         // of each thread
   float *sq = smf + L::kQ, *sp = smf + L::kP;
-  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const int tid = threadIdx.x, ty = tid >> 3, tx = tid & 7;
   const int h = un.h, r0 = un.r0, nrows = un.nrows, n = un.n, first_pos = un.first_pos;
   const int slot = un.slot, piece = un.piece, pieces = un.pieces;
   const int* pages = un.pages;
@@ -79,7 +82,7 @@ __device__ __forceinline__ void simt_unit(const PrefixParams& p, const SimtUnit&
     return (long long)(rr >> p.g_shift) * p.Hq + h * p.G + (rr & (p.G - 1));
   };
   float m[TM], l[TM];
-  uint64_t acc[TM][DC * 2];  // columns tx * 4 + 64 c .. in pairs
+  uint64_t acc[TM][DC * 2];  // columns tx * 4 + 32 c .. in pairs
 #pragma unroll
   for (int a = 0; a < TM; ++a) {
     m[a] = -INFINITY;
@@ -142,17 +145,17 @@ __device__ __forceinline__ void simt_unit(const PrefixParams& p, const SimtUnit&
       read_ids(tile + 2);
     }
     const float *sk = smf + L::kKV + (tile & 1) * 2 * L::kTile, *sv = sk + L::kTile;
-    // keys tx + 16 e of the tile that exist: in range, on a page of the pool
+    // keys tx + 8 e of the tile that exist: in range, on a page of the pool
     uint32_t live = 0;
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
-      const int j = j0 + tx + 16 * e;
+      const int j = j0 + tx + 8 * e;
       if (j < n) {
         const int id = pages[j >> p.page_shift];
         if (id >= 0 && id < p.num_pages) live |= 1u << e;
       }
     }
-    // scores of keys tx + 16 e, two columns in a packed FMA
+    // scores of rows ty + 16 a and keys tx + 8 e, two columns in a packed FMA
     uint64_t s2[TM][NE];
 #pragma unroll
     for (int a = 0; a < TM; ++a)
@@ -163,10 +166,10 @@ __device__ __forceinline__ void simt_unit(const PrefixParams& p, const SimtUnit&
       ulonglong2 kk[NE];
 #pragma unroll
       for (int e = 0; e < NE; ++e)
-        kk[e] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * e) * L::kLd + c);
+        kk[e] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 8 * e) * L::kLd + c);
 #pragma unroll
       for (int a = 0; a < TM; ++a) {
-        const ulonglong2 qq = *reinterpret_cast<const ulonglong2*>(sq + (ty * TM + a) * L::kLd + c);
+        const ulonglong2 qq = *reinterpret_cast<const ulonglong2*>(sq + (ty + 16 * a) * L::kLd + c);
 #pragma unroll
         for (int e = 0; e < NE; ++e)
           s2[a][e] = tc::fma_f2(qq.y, kk[e].y, tc::fma_f2(qq.x, kk[e].x, s2[a][e]));
@@ -184,17 +187,17 @@ __device__ __forceinline__ void simt_unit(const PrefixParams& p, const SimtUnit&
     bool hides = false;  // a row of the thread does not see a key of the tile that exists
 #pragma unroll
     for (int a = 0; a < TM; ++a) {
-      const int last = first_pos + ((ty * TM + a) >> p.g_shift);
+      const int last = first_pos + ((ty + 16 * a) >> p.g_shift);
       float top = -INFINITY;
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
-        const bool sees = j0 + tx + 16 * e <= last;
+        const bool sees = j0 + tx + 8 * e <= last;
         hides |= !sees && ((live >> e) & 1);
         if (!((live >> e) & 1) || !sees) s[a][e] = -INFINITY;
         top = fmaxf(top, s[a][e]);
       }
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const float m_new = fmaxf(m[a], top);
       const float base = m_new == -INFINITY ? 0.f : m_new;
       const float corr = exp2f(m[a] - base);
@@ -203,24 +206,23 @@ __device__ __forceinline__ void simt_unit(const PrefixParams& p, const SimtUnit&
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
         const float pe = exp2f(s[a][e] - base);
-        sp[(ty * TM + a) * L::kLdP + tx + 16 * e] = pe;
+        sp[(ty + 16 * a) * L::kLdP + tx + 8 * e] = pe;
         sum += pe;
       }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l[a] = l[a] * corr + sum;
+      l[a] = l[a] * corr + sum;  // of the thread's keys
 #pragma unroll
       for (int c = 0; c < DC * 2; ++c) acc[a][c] = tc::mul_f2(acc[a][c], tc::pack_f2(corr, corr));
     }
-    // a row's P is written and read by the 16 threads of its half warp
+    // a row's P is written and read by 8 threads of one warp
     const bool careful = __any_sync(0xffffffffu, hides);
+    __syncwarp();
     auto product = [&](auto check) {
 #pragma unroll 2
       for (int j = 0; j < L::kKeys; j += 4) {
         float pj[TM][4];
 #pragma unroll
         for (int a = 0; a < TM; ++a) {
-          const float4 t = *reinterpret_cast<const float4*>(sp + (ty * TM + a) * L::kLdP + j);
+          const float4 t = *reinterpret_cast<const float4*>(sp + (ty + 16 * a) * L::kLdP + j);
           pj[a][0] = t.x; pj[a][1] = t.y; pj[a][2] = t.z; pj[a][3] = t.w;
         }
 #pragma unroll
@@ -228,7 +230,7 @@ __device__ __forceinline__ void simt_unit(const PrefixParams& p, const SimtUnit&
 #pragma unroll
           for (int c = 0; c < DC; ++c) {
             const ulonglong2 vv =
-                *reinterpret_cast<const ulonglong2*>(sv + (j + e) * L::kLd + tx * 4 + 64 * c);
+                *reinterpret_cast<const ulonglong2*>(sv + (j + e) * L::kLd + tx * 4 + 32 * c);
 #pragma unroll
             for (int a = 0; a < TM; ++a) {
               const float w = pj[a][e];
@@ -245,21 +247,23 @@ __device__ __forceinline__ void simt_unit(const PrefixParams& p, const SimtUnit&
   }
 #pragma unroll
   for (int a = 0; a < TM; ++a) {
-    const int r = ty * TM + a;
+    const int r = ty + 16 * a;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) l[a] += __shfl_xor_sync(0xffffffffu, l[a], o);
     if (r >= nrows) continue;
     const long long at = (long long)slot * rows + row_id(r);
     if (tx == 0) p.part_ml[at] = make_float2(m[a], l[a]);
     if (l[a] == 0.f) continue;  // no key (scores of NaN leave the maximum at -inf and l at NaN)
 #pragma unroll
     for (int c = 0; c < DC; ++c)
-      *reinterpret_cast<ulonglong2*>(p.part_o + at * D + tx * 4 + 64 * c) =
+      *reinterpret_cast<ulonglong2*>(p.part_o + at * D + tx * 4 + 32 * c) =
           make_ulonglong2(acc[a][2 * c], acc[a][2 * c + 1]);
   }
 }
 
 // RG1 rows a tile of the packed rows against the prefix, RG2 of a request against its own keys
 template <int D, int RG1, int RG2>
-__global__ void __launch_bounds__(kPsThreads) prefix_simt_kernel(const PrefixParams p,
+__global__ void __launch_bounds__(kPsThreads, 2) prefix_simt_kernel(const PrefixParams p,
                                                                  const SimtGrid g) {
   extern __shared__ __align__(16) float smf[];
   pdl_wait();

@@ -41,7 +41,7 @@ struct SimtSmem {
 
 struct SimtGrid {
   int units1;  // CTAs of the prefix: tiles of packed rows x kv heads x pieces
-  int tiles2;  // row tiles of a request
+  int tiles2;  // places of request tiles (pa_place)
 };
 
 // The rows and keys of a CTA.
@@ -286,9 +286,12 @@ __global__ void __launch_bounds__(kPsThreads, 2) prefix_simt_kernel(const Prefix
     u -= g.units1;
     un.piece = u % p.ns2;
     u /= p.ns2;
-    un.h = u % p.Hk;
-    u /= p.Hk;
-    const int tile = u % g.tiles2, b = u / g.tiles2;
+    un.h = u / g.tiles2;
+    u %= g.tiles2;
+    constexpr int kShift = RG2 == 64 ? 6 : 4;
+    const int2 place = pa_place(p, u, kShift);
+    const int tile = place.y, b = max(place.x, 0);
+    if (place.x < 0 || tile < 0) return;
     const PaRequest r = pa_request(p, b);
     un.r0 = r.t0 * p.G + tile * RG2;
     un.nrows = min(RG2, min(r.nq, p.max_q) * p.G - tile * RG2);
@@ -331,7 +334,7 @@ constexpr long long kPrefixTiles = 4 * kRowsCtas;
 // Which kernel does which part.
 struct PrefixPlan {
   int rg1, rg2;            // rows of a CUDA-core tile: packed (prefix), of a request (own keys)
-  int simt1, simt2;        // such tiles; 0: not its part
+  int simt1, simt2;        // such tiles, and places of such tiles (pa_place); 0: not its part
   int tc1, tc2;            // 256-row tiles on the tensor cores, the same way
   bool fused, direct;      // request tiles take the prefix too; one piece in all, no merge
   bool cluster;            // few-rows kernel as one cluster per kv head, which joins the pieces itself
@@ -355,7 +358,7 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
     // a tile on average keep their rows to themselves: prefix and own keys in one pass.  Below that
     // the padding would cost more than the merge.
     w.fused = rows >= 64LL * B;
-    w.tc2 = tiles(rows_q, 256);
+    w.tc2 = (int)pa_places(T, B, G, 8);
     if (!w.fused && prefix_len) w.tc1 = tiles(rows, 256);
   } else if (dt == BSA_BF16) {
     // Up to 64 rows share an own key: the few-rows kernel.  It takes the prefix too where all rows
@@ -380,18 +383,18 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
     w.rg2 = rows_q <= 16 ? 16 : 64;
     w.rg1 = w.rg2 == 64 || rows > 32 ? 64 : rows > 16 ? 32 : 16;
     w.simt1 = prefix_len ? tiles(rows, w.rg1) : 0;
-    w.simt2 = keys2 ? tiles(rows_q, w.rg2) : 0;
+    w.simt2 = keys2 ? (int)pa_places(T, B, G, w.rg2 == 64 ? 6 : 4) : 0;
   }
   if (w.tc1) w.ns1 = pieces_for((long long)w.tc1 * Hk, kSMs, (prefix_len + 127) / 128, 4);
   // Two CTAs per SM: half for the prefix, unless the own keys fill the GPU by themselves.
   if (w.simt1)
     w.ns1 = pieces_for((long long)w.simt1 * Hk,
-                       (long long)w.simt2 * B * Hk > 2 * kSMs ? 2 * kSMs : kSMs,
+                       (long long)w.simt2 * Hk > 2 * kSMs ? 2 * kSMs : kSMs,
                        tiles(prefix_len, 4096 / d), 2);
   if (w.tc2)
     w.ns2 = pieces_for((rows + 255) / 256 * Hk, kSMs,
                        (keys2 + (w.fused ? prefix_len : 0) + 127) / 128, 4);
-  if (w.simt2) w.ns2 = pieces_for((long long)w.simt2 * B * Hk, kSMs, tiles(keys2, 4096 / d), 2);
+  if (w.simt2) w.ns2 = pieces_for((long long)w.simt2 * Hk, kSMs, tiles(keys2, 4096 / d), 2);
   w.direct = w.tc2 && !w.tc1 && w.ns2 == 1;
   const long long all = w.direct ? 0 : (long long)T * Hq * (w.ns1 + w.ns2);
   w.ml_bytes = align_up((size_t)all * sizeof(float2), 256);
@@ -410,7 +413,7 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
 template <int D, int RG1, int RG2>
 bsa_status launch_simt(const PrefixParams& p, const PrefixPlan& w, cudaStream_t st) {
   const long long units1 = (long long)w.simt1 * p.Hk * p.ns1;
-  const long long units2 = (long long)p.B * w.simt2 * p.Hk * p.ns2;
+  const long long units2 = (long long)w.simt2 * p.Hk * p.ns2;
   if (units1 + units2 > INT_MAX) return BSA_ERR_UNSUPPORTED;
   if (units1 + units2 == 0) return BSA_OK;
   const int smem = std::max(SimtSmem<D, RG1>::kTotal, SimtSmem<D, RG2>::kTotal);
@@ -443,6 +446,8 @@ bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status,
              ? BSA_OK
              : BSA_ERR_CUDA;
 }
+
+constexpr int kMaxKeys = INT_MAX - 1024;  // room to round up to tiles
 
 bool sizes_ok(int T, int B, int Hq, int Hk, int d, int page, int table_ld, int prefix_len,
               int max_q) {
@@ -486,7 +491,8 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
   BSA_REQUIRE(group_ok(Hq, Hk) && head_dim_ok(d) && page_ok(page), BSA_ERR_UNSUPPORTED);
   // rows of the pool and of the packed queries, and a request's tokens, are 32-bit
   BSA_REQUIRE((long long)num_pages * Hk * page <= INT_MAX && (long long)T * Hq <= INT_MAX &&
-                  (long long)table_ld * page <= INT_MAX, BSA_ERR_UNSUPPORTED);
+                  (long long)T + B <= INT_MAX && prefix_len <= kMaxKeys &&
+                  (long long)table_ld * page <= kMaxKeys, BSA_ERR_UNSUPPORTED);
   BSA_REQUIRE(T <= 1 || q_stride >= (long long)Hq * d, BSA_ERR_SHAPE);
   const int es = dt == BSA_BF16 ? 2 : 4;
   BSA_REQUIRE(all_aligned16(q, k_pages, v_pages, o) && (T <= 1 || q_stride * es % 16 == 0),

@@ -83,6 +83,29 @@ __device__ __forceinline__ long long pa_piece_row(const PrefixParams& p, bool pr
          (p.cluster ? (long long)h * (p.B + p.item_ctas) + i : (long long)i * p.Hk + h) *
              p.own_rows + (long long)c * p.own_rows;
 }
+// Row tiles of the requests, 1 << shift rows each, as places in a row: request b's start at (its first
+// packed row >> shift) + b, which leaves room for a last, partly filled one each, so (T * G >> shift) +
+// B places hold them all however the tokens are spread.
+inline long long pa_places(int T, int B, int G, int shift) {
+  return ((long long)T * G >> shift) + B;
+}
+// The request of a place and the tile of it (b = -1: none); all lanes of a warp take part.
+__device__ __forceinline__ int2 pa_place(const PrefixParams& p, int place, int shift) {
+  auto start = [&](int b) {
+    return ((min(max(p.cu_q ? p.cu_q[b] : b, 0), p.T) << p.g_shift) >> shift) + b;
+  };
+  int n = 0;
+#pragma unroll 4
+  for (int i = 0; i < p.B; i += 32) {
+    const int b = i + (threadIdx.x & 31);
+    n += __popc(__ballot_sync(0xffffffffu, b < p.B && start(b) <= place));
+  }
+  return n ? make_int2(n - 1, place - start(n - 1)) : make_int2(-1, 0);
+}
+// bf16 pairs: the sign bit of each half that holds an infinity or NaN
+__device__ __forceinline__ uint32_t pa_nonfinite(uint32_t w) {
+  return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
 // New tokens in all: rows at or after this are left as they were.
 __device__ __forceinline__ int pa_tokens(const PrefixParams& p) {
   return p.cu_q ? min(max(p.cu_q[p.B], 0), p.T) : p.B;

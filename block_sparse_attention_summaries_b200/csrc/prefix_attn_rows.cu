@@ -93,6 +93,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
+// Adds the infinities and NaNs of V at own keys [j0, n), D / 4 columns from col, to the rows that see
+// them: a warp, which has written those columns.  Not inline: it runs for bad values only.
+template <int D>
+__device__ __noinline__ void add_cleaned(const __nv_bfloat16* v, const int* pages, int num_pages,
+                                         int page_shift, int Hk, int h, int j0, int n,
+                                         int first_pos, int nrows, int g_shift, float* out,
+                                         int col) {
+  for (int i = threadIdx.x & 31; i < nrows * (D / 4); i += 32) {
+    const int row = i / (D / 4), c = col + i % (D / 4);
+    const int end = min(n, first_pos + (row >> g_shift) + 1);
+    float add = 0.f;
+    for (int j = j0; j < end; ++j) {
+      const int pg = pages[j >> page_shift];
+      if (pg < 0 || pg >= num_pages) continue;
+      const float f = __bfloat162float(
+          v[((((long long)pg * Hk + h) << page_shift) + (j & ((1 << page_shift) - 1))) * D + c]);
+      if (!isfinite(f)) add += f;
+    }
+    if (add != 0.f) out[row * D + c] += add;
+  }
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(kRThreads, 2)
     prefix_rows_kernel(const __grid_constant__ CUtensorMap tmq,
@@ -314,6 +336,7 @@ __global__ void __launch_bounds__(kRThreads, 2)
     // one row tile keeps its queries in registers; more read them from shared memory for each tile
     uint32_t q[MT == 1 ? D / 16 : 1][4];
     float acc[MT][NT][4], m[MT][2], l[MT][2];
+    int dirty = INT_MAX;  // first key of a tile whose V was cleaned, in this piece
     int k = 0;
     for (int i = 0; i < count; ++i, k += 2) {
       const int buf = i & 1;
@@ -349,6 +372,7 @@ __global__ void __launch_bounds__(kRThreads, 2)
           m[mt][0] = m[mt][1] = -INFINITY;
           l[mt][0] = l[mt][1] = 0.f;
         }
+        dirty = INT_MAX;
       }
       const uint32_t kt = base + ks * L::kTile, vt = base + vs * L::kTile;
       // scores of keys 8 NS warp .. of the tile
@@ -449,6 +473,27 @@ __global__ void __launch_bounds__(kRThreads, 2)
         }
       }
       bar_consumers();
+      // some row sees the tile in part: an infinity or NaN behind its position must not reach it as
+      // 0 x NaN; it is zeroed here and added at the end to the rows that see it
+      if (t.j0 + min(left, kRKeys) - 1 > t.first_pos) {
+        uint32_t found = 0;
+        constexpr int NC = D / 32;  // 16-byte chunks of the warp's columns
+        for (int e = lane; e < kRKeys * NC; e += 32) {
+          const int ch = warp * NC + e % NC;
+          uint32_t* w = reinterpret_cast<uint32_t*>(smem + vs * L::kTile + (ch >> 3) * L::kHalf +
+                                                    tc::sw128_offset(e / NC, ch & 7));
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            // keys that do not exist are masked below
+            const uint32_t bad = pa_nonfinite(w[f]);
+            if (bad) w[f] &= ~((bad >> 15) * 0xffffu);
+            if (is_key(e / NC)) found |= bad;
+          }
+        }
+        fence_proxy_async();  // the next copy into the slot comes after these writes
+        if (__any_sync(0xffffffffu, found != 0)) dirty = min(dirty, t.j0);
+        __syncwarp();
+      }
 #pragma unroll
       for (int kk = 0; kk < kRKeys / 16; ++kk) {
         uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
@@ -510,6 +555,13 @@ __global__ void __launch_bounds__(kRThreads, 2)
               *reinterpret_cast<float2*>(op + 8 * c) =
                   make_float2(acc[mt][c][2 * a], acc[mt][c][2 * a + 1]);
           }
+        if (dirty < INT_MAX) {
+          __syncwarp();
+          add_cleaned<D>(static_cast<const __nv_bfloat16*>(p.v),
+                         p.table + (size_t)t.i * p.table_ld, p.num_pages, p.page_shift, p.Hk, t.h,
+                         dirty, min(t.n, t.j0 + kRKeys), t.first_pos, t.nrows, p.g_shift,
+                         p.item_o + slot * D, warp * (D / 4));
+        }
       }
     }
   }

@@ -15,10 +15,12 @@
 // 512 clocks of tensor work at d = 128: long units are bound by the exponentials and the FMAs around
 // them, short batches (packed rows up to about 256) by HBM.
 //   warps 0-3, 4-7: softmax of stream 0, 1 (a thread owns a row: TMEM lane = row)
-//   warp 8: TMA producer; lane i loads box i (a page, or 128 rows of one) of K and V into a ring
-//   warp 9: MMA issuer (lane 0); all its lanes zero the V rows behind the last key, because
-//           0 x NaN of a place never written would reach the row
-//   warps 10, 11: none (they complete the helper warpgroup, whose registers the softmax takes)
+//   warp 8: TMA producer; lane i loads box i (a page, or 128 rows of one) of K and V into a ring.  It
+//           mends tiles of V that hold what a row must not see, because 0 x NaN would reach it: rows
+//           behind the last key, infinities and NaNs of tiles on the diagonal
+//   warp 9: MMA issuer (one elected lane)
+//   warp 10: adds such infinities and NaNs in the end to the rows that do see them
+//   warp 11: none (it completes the helper warpgroup, whose registers the softmax takes)
 // P is written over S in TMEM and read from there as the A operand.  S_s of step i + 1 is issued
 // behind P V_s of step i, so its completion also says that O_s may be rescaled (lazily: only when a
 // row's maximum rises by more than 2^8, else the old maximum stays and P just exceeds 1).
@@ -42,6 +44,7 @@ constexpr float kXRescale = 8.f;  // log2 units
 // P goes to the tensor cores in two parts: the product with V of the first kXFirst keys runs while
 // the last exponentials are computed
 constexpr int kXFirst = 64;
+constexpr int kXMend = 8;         // mended tiles under way: more than the ring holds
 constexpr int kXMasks = 8;        // key tiles whose page masks are kept: more than the ring holds
 
 template <int D>
@@ -56,7 +59,7 @@ struct TcSmem {
 struct TcGrid {
   int units1;   // CTAs over packed rows
   int tiles1;   // 256-row tiles of the packed rows
-  int tiles2;   // of a request
+  int tiles2;   // places of request tiles (pa_place)
   int fused;    // request units take the prefix too
   int direct;   // one piece in all: o and lse are written here
   int boxes;    // boxes of a key tile (128 / rows of a box)
@@ -124,6 +127,29 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Infinities and NaNs of a tile of V ([halves][128 x 128 B]) to zero; whether there were any.
+__device__ __forceinline__ bool clean_tile(unsigned char* vt, int halves, int lane) {
+  // a multiply by zero keeps them and nothing else
+  __nv_bfloat162 found = __floats2bfloat162_rn(0.f, 0.f);
+  const __nv_bfloat162 zero = found;
+  const int n = halves * 128 * 8;
+#pragma unroll 4
+  for (int i = lane; i < n; i += 32) {
+    const uint4 v = reinterpret_cast<const uint4*>(vt)[i];
+    found = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.x), zero, found);
+    found = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.y), zero, found);
+    found = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.z), zero, found);
+    found = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.w), zero, found);
+  }
+  const bool dirty = pa_nonfinite(*reinterpret_cast<const uint32_t*>(&found)) != 0;
+  if (!__any_sync(0xffffffffu, dirty)) return false;
+  for (int i = lane; i < 4 * n; i += 32) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(vt) + i;
+    *w &= ~((pa_nonfinite(*w) >> 15) * 0xffffu);
+  }
+  return true;
+}
+
 // What a CTA works on.
 struct Unit {
   int t0, r0;        // first token; first row among the packed rows (t0 * G)
@@ -157,14 +183,13 @@ __device__ __forceinline__ Unit unit_of(const PrefixParams& p, const TcGrid& g) 
     i -= g.units1;
     piece = i % p.ns2;
     i /= p.ns2;
-    const int tile = i % g.tiles2;
-    i /= g.tiles2;
-    const int b = i % p.B;
-    u.h = i / p.B;
+    const int2 place = pa_place(p, i % g.tiles2, 8);
+    const int b = max(place.x, 0), tile = place.y;
+    u.h = i / g.tiles2;
     const PaRequest r = pa_request(p, b);
     u.t0 = r.t0 + tile * (256 >> p.g_shift);
     u.r0 = u.t0 * p.G;
-    u.nrows = min(256, min(r.nq, p.max_q) * p.G - tile * 256);
+    u.nrows = place.x < 0 || tile < 0 ? 0 : min(256, min(r.nq, p.max_q) * p.G - tile * 256);
     u.first_pos = r.len - r.nq + tile * (256 >> p.g_shift);
     u.n0 = g.fused ? p.prefix_len : 0;
     u.n1 = max(0, min(r.len, u.first_pos + ((u.nrows - 1) >> p.g_shift) + 1));
@@ -180,6 +205,32 @@ __device__ __forceinline__ Unit unit_of(const PrefixParams& p, const TcGrid& g) 
   return u;
 }
 
+// Adds the infinities and NaNs of V at own keys [j0, n) to the results (o, or else part) of the rows
+// that see them: a warp.  Not inline and by value, so that it takes no register of the other roles.
+template <int D>
+__device__ __noinline__ void add_cleaned(const __nv_bfloat16* v, const int* pages, int num_pages,
+                                         int page_shift, int Hk, int h, int j0, int n,
+                                         int first_pos, int r0, int nrows, int g_shift, int Hq,
+                                         __nv_bfloat16* o, float* part) {
+  for (int i = threadIdx.x & 31; i < nrows * D; i += 32) {
+    const int row = i / D, c = i % D, rr = r0 + row;
+    const int end = min(n, first_pos + (row >> g_shift) + 1);
+    float add = 0.f;
+    for (int j = j0; j < end; ++j) {
+      const int pg = pages[j >> page_shift];
+      if (pg < 0 || pg >= num_pages) continue;
+      const float f = __bfloat162float(
+          v[((((long long)pg * Hk + h) << page_shift) + (j & ((1 << page_shift) - 1))) * D + c]);
+      if (!isfinite(f)) add += f;
+    }
+    if (add == 0.f) continue;
+    const long long at = ((long long)(rr >> g_shift) * Hq + (h << g_shift) +
+                          (rr & ((1 << g_shift) - 1))) * D + c;
+    if (o) o[at] = __float2bfloat16_rn(__bfloat162float(o[at]) + add);
+    else part[at] += add;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kXThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmq,
@@ -190,7 +241,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_align1024(smem_raw);
-  __shared__ __align__(8) uint64_t bars[2 * L::kSlots + kXMasks + 9];
+  __shared__ __align__(8) uint64_t bars[2 * L::kSlots + kXMasks + 9 + kXMend];
   uint64_t* full = bars;
   uint64_t* empty = full + L::kSlots;
   uint64_t* mask_full = empty + L::kSlots;  // page mask of a key tile written
@@ -198,8 +249,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
   uint64_t* s_full = q_full + 1;  // [2]
   uint64_t* p_full = s_full + 2;  // [stream][part]
   uint64_t* o_done = p_full + 4;  // [2]
+  uint64_t* mended = o_done + 2;  // V of a tile is fit for its product
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ int s_dirty;  // first own key of a tile of V that was cleaned
   __shared__ uint32_t s_mask[kXMasks];  // boxes of the key tile that are on pages of the pool
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -237,6 +290,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kXMasks; ++i) mbar_init(&mask_full[i], 1);
+    for (int i = 0; i < kXMend; ++i) mbar_init(&mended[i], 1);
     mbar_init(q_full, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
@@ -246,6 +300,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     }
     fence_mbar_init();
     s_abort = 0;
+    s_dirty = INT_MAX;
   }
   if (warp == 9) {
     tc::tmem_alloc(&s_tmem, 512);
@@ -263,6 +318,21 @@ __global__ void __launch_bounds__(kXThreads, 1)
   auto s_col = [&](int s) { return tmem + (uint32_t)(s * 128); };
   auto o_col = [&](int s) { return tmem + 256u + (uint32_t)(s * 128); };
   auto slot_at = [&](int i) { return smem + L::kRing + i * L::kTile; };
+  // Tile ti of the piece needs its V mended before a product: rows without a key (the rest of a last
+  // tile, pages outside the pool), or keys that some row does not see.
+  auto j0_at = [&](int ti) {  // its first key
+    const int t = u.tile0 + ti;
+    return (t >= u.tiles0 ? t - u.tiles0 : t) * kXKeys;
+  };
+  auto left_at = [&](int ti) {  // keys from there on
+    return (u.tile0 + ti >= u.tiles0 ? u.n1 : u.n0) - j0_at(ti);
+  };
+  auto partly = [&](int ti) {
+    return u.tile0 + ti >= u.tiles0 && j0_at(ti) + min(left_at(ti), kXKeys) - 1 > u.first_pos;
+  };
+  auto mends = [&](int ti) {
+    return left_at(ti) < kXKeys || s_mask[ti % kXMasks] != (1u << g.boxes) - 1u || partly(ti);
+  };
   const uint32_t all_boxes = (1u << g.boxes) - 1u;
 
   if (warp >= 8) {
@@ -287,7 +357,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     };
     const uint32_t box_bytes = (uint32_t)(128 << g.box_shift);  // of one 64-column half
     int next = page_of(u.tile0);
-    int k = 0;  // ring position
+    int k = 0, nmend = 0;  // ring position, mended tiles
     bool ok = true;
     for (int i = 0; i < nt && ok; ++i) {
       const int t = u.tile0 + i, id = next;
@@ -312,6 +382,29 @@ __global__ void __launch_bounds__(kXThreads, 1)
             tc::tma_load_2d(slot_at(sl) + hf * 16384 + lane * box_bytes, kv ? &tmv : &tmk, hf * 64,
                             y, &full[sl]);
       }
+      if (!ok || !mends(i)) continue;
+      // the tile's V, once it is there
+      const int kv = k - 1, sl = kv % L::kSlots;
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[sl], (kv / L::kSlots) & 1));
+      if (!ok) break;
+      unsigned char* vt = slot_at(sl);
+      const int j0 = j0_at(i), left = left_at(i);
+      for (int r = lane; r < kXKeys; r += 32) {
+        if (r < left && ((have >> (r >> g.box_shift)) & 1)) continue;
+        for (int hf = 0; hf < kHalves; ++hf)
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(vt + hf * 16384 + r * 128 + c * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+      }
+      __syncwarp();
+      // an infinity or NaN behind a row's position must not reach it as 0 x NaN: it is zeroed here,
+      // and added in the end to the rows that do see it
+      if (partly(i) && clean_tile(vt, kHalves, lane) && lane == 0) s_dirty = min(s_dirty, j0);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mended[nmend % kXMend]);
+      ++nmend;
     }
     if (!ok && lane == 0) s_abort = 1;
     // copies still in flight land before the CTA leaves, whatever the other roles do
@@ -347,6 +440,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       return true;
     };
     bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_full, 0));
+    int nmend = 0;
     for (int s = 0; s < 2 && ok; ++s)
       if (steps(s) > 0) ok = issue_s(s, 0);
     for (int i = 0; i < steps(0) && ok; ++i) {
@@ -356,25 +450,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
         const int ti = tile_at(s, i), k = 2 * ti + 1, sl = k % L::kSlots;
         ok = ready(k);
         if (!ok) continue;
-        // rows of V without a key, once per tile
-        if (!wide || s == 0) {
-          const int t = u.tile0 + ti;
-          const bool own = t >= u.tiles0;
-          const int left = (own ? u.n1 : u.n0) - (own ? t - u.tiles0 : t) * kXKeys;
-          const uint32_t have = s_mask[ti % kXMasks];
-          if (left < kXKeys || have != all_boxes) {
-            unsigned char* vt = slot_at(sl);
-            for (int r = lane; r < kXKeys; r += 32) {
-              if (r < left && ((have >> (r >> g.box_shift)) & 1)) continue;
-              for (int hf = 0; hf < kHalves; ++hf)
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  *reinterpret_cast<uint4*>(vt + hf * 16384 + r * 128 + c * 16) =
-                      make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async();
-            __syncwarp();
-          }
+        // a tile of V that the producer mends first, once per tile
+        if ((!wide || s == 0) && mends(ti)) {
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&mended[nmend % kXMend],
+                                                         (nmend / kXMend) & 1));
+          ++nmend;
+          if (!ok) continue;
         }
         const uint32_t b = desc_lo(ring + sl * L::kTile, 16384);
 #pragma unroll
@@ -397,6 +478,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
     commit_one(leader, smem_u32(q_full));
     ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_full, 1)) && ok;
     if (!ok && lane == 0) s_abort = 1;
+  } else if (warp == 10) {
+    // ------------------------------------- adds what was cleaned to the rows that do see it
+    asm volatile("bar.sync 2, 288;" ::: "memory");  // the results are written
+    const int j0 = *(volatile int*)&s_dirty;
+    if (j0 < INT_MAX)
+      add_cleaned<D>(static_cast<const __nv_bfloat16*>(p.v), u.own, p.num_pages, p.page_shift, p.Hk,
+                     u.h, j0, min(u.n1, (u.tile1 - u.tiles0) * kXKeys), u.first_pos, u.r0, u.nrows,
+                     p.g_shift, p.Hq, g.direct ? static_cast<__nv_bfloat16*>(p.o) : nullptr,
+                     p.part_o + (size_t)u.slot * rows * D);
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kXRegsSoftmax));
@@ -425,7 +515,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
       // columns of the tile the row sees: [0, hi), on pages of the pool
       const bool own = t >= u.tiles0;
       const int j0 = (own ? t - u.tiles0 : t) * kXKeys;
-      const int hi = (own ? min(u.n1, pos + 1) : u.n0) - j0;
+      const int hi =
+          (own ? min(u.n1, pos + 1) : u.n0) - j0;
       if (!__all_sync(0xffffffffu, hi >= kXKeys && have == all_boxes)) {
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -582,6 +673,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       }
       __syncwarp();
     }
+    asm volatile("bar.arrive 2, 288;" ::: "memory");
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -650,12 +742,12 @@ bool prefix_kv_map(CUtensorMap* m, const void* pool, const PrefixParams& p, int 
 }
 
 // The units of a plan on the tensor cores: packed rows x prefix (tiles1 > 0, p.ns1 pieces) and
-// requests x own keys (tiles2 > 0, p.ns2 pieces; `fused`: prefix and own keys).
+// requests x own keys (tiles2 > 0 places, p.ns2 pieces; `fused`: prefix and own keys).
 bsa_status prefix_attn_tc(const PrefixParams& p, int d, int tiles1, int tiles2, bool fused,
                           bool direct, int* status, cudaStream_t st) {
   TcGrid g;
   const long long units1 = (long long)tiles1 * p.Hk * p.ns1;
-  const long long units2 = (long long)tiles2 * p.B * p.Hk * p.ns2;
+  const long long units2 = (long long)tiles2 * p.Hk * p.ns2;
   if (units1 + units2 > INT_MAX) return BSA_ERR_UNSUPPORTED;
   if (units1 + units2 == 0) return BSA_OK;
   g.units1 = (int)units1;

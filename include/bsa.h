@@ -580,7 +580,8 @@ bsa_status bsa_paged_append(const void* k, const void* v, bsa_dtype dt, int T, i
  *             initialisation and may be reused once the stream has passed the call.  Calls that
  *             share one must not run at the same time.
  * Keys and values that no position reaches (the rest of a last page, other pages of the pool) are
- * not used, whatever they hold.  A page id outside the pool is not read: its tokens take no part.
+ * not used, whatever they hold, and an infinity or NaN in a key or value reaches the tokens that see
+ * it and no others.  A page id outside the pool is not read: its tokens take no part.
  * Sums, softmax statistics and partial results are float32; with bf16 inputs the softmax weights
  * are rounded to bf16 for the product with V.  Limits: num_pages * Hk * page and T * Hq < 2^31.
  */

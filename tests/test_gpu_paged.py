@@ -243,6 +243,36 @@ def test_nonfinite_rows_stay_where_they_are(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,n,at,prefix", [(6, 50, 46, 200), (30, 90, 70, 0), (100, 300, 250, 130),
+                                            (400, 400, 37, 5), (400, 700, 690, 300)])
+def test_nonfinite_values_reach_only_rows_that_see_them(dtype, d, nq, n, at, prefix):
+    """An infinity and a NaN in V at own position `at`: earlier rows are as without them, later ones
+    hold them in the columns concerned and are as without them in the others."""
+    m = Batch(16, dtype, 8, 2, d, 16, prefix, [1, nq, 2], [9, n, 30])
+    clean, clean_lse = m.run()
+    page, off = int(m.own_ids[1][at // 16]), at % 16
+    m.v[page, 0, off, 3] = float("inf")
+    m.v[page, 1, off, d - 1] = float("nan")
+    if at + 1 < n - 1:  # a second one, seen by fewer rows
+        page, off = int(m.own_ids[1][(at + 1) // 16]), (at + 1) % 16
+        m.v[page, 0, off, 20] = float("-inf")
+    o, lse = m.run()
+    assert torch.equal(lse, clean_lse)
+    t = torch.arange(o.shape[0], device=DEV)[:, None, None]
+    pos = torch.where((t >= 1) & (t < 1 + nq), n - nq + t - 1, -1)  # own position, request 1
+    h = torch.arange(8, device=DEV)[None, :, None]
+    c = torch.arange(d, device=DEV)[None, None, :]
+    inf = (pos >= at) & (h < 4) & (c == 3)
+    nan = (pos >= at) & (h >= 4) & (c == d - 1)
+    neg = (pos >= at + 1) & (h < 4) & (c == 20) & (at + 1 < n - 1)
+    assert (o[inf] == float("inf")).all() and torch.isnan(o[nan]).all()
+    assert (o[neg] == float("-inf")).all()
+    rest = ~(inf | nan | neg)
+    assert inf.any() and torch.equal(o[rest], clean[rest])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_tokens_beyond_max_q_are_left(dtype):
     m = Batch(10, dtype, 8, 2, 64, 16, 50, [3, 9, 2], [30, 40, 2])
     o = torch.full(m.q.shape, 7.0, device=DEV, dtype=dtype)
@@ -604,6 +634,65 @@ def test_captured_decode_steps():
             want, tol = s.want(b, q[i:i + 1])
             assert ((o[i:i + 1].double() - want).abs() <= tol).all()
     assert int(s.status) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("decode", [True, False])
+def test_captured_long_batches(dtype, decode):
+    """A captured call with many key pieces, replayed on other lengths, queries and cache contents."""
+    nq = [1] * 40 if decode else [3, 200, 1, 1, 90]
+    lens = [(53 * i) % 400 + 1 for i in range(40)] if decode else [40, 260, 5, 1, 90]
+    m = Batch(17, dtype, 8, 2, 128, 32, 6000, nq, lens, decode=decode, spare_ld=1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        m.run()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = m.run()
+    for step in range(3):
+        g.replay()
+        m.check(o, lse, requests=[0, 1, 4])
+        m.q.copy_(torch.randn_like(m.q))
+        m.v.nan_to_num_().mul_(0.5)
+        m.lens_list = [max(q, n - 7 * (step + 1)) for q, n in zip(nq, lens)]
+        m.lens.copy_(i32(m.lens_list))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_long_prompt_among_many(dtype):
+    """A prompt beside 300 requests of one token: row tiles go by the tokens there are."""
+    nq = [1] * 150 + [700] + [1] * 150
+    m = Batch(18, dtype, 4, 2, 64, 16, 90, nq, [n + 10 for n in nq])
+    m.check(*m.run(), requests=[0, 149, 150, 151, 300])
+
+
+def test_far_pages():
+    """Pages behind the first 2^31 elements of the pool, in all three operators."""
+    P, Hk, page, d = 270_000, 1, 64, 128  # 2.2e9 elements
+    k = torch.empty(P, Hk, page, d, device=DEV, dtype=BF16)
+    v = torch.empty(P, Hk, page, d, device=DEV, dtype=BF16)
+    pk, pv = (torch.randn(130, Hk, d, device=DEV).to(BF16) for _ in range(2))
+    ids = i32([P - 1, 5, P - 3])
+    at = (ids.long()[torch.arange(130, device=DEV) // 64] * 64
+          + torch.arange(130, device=DEV) % 64).int()
+    bsa.paged_append(pk, pv, at, k, v)
+    assert torch.equal(k[P - 1, 0, :], pk[:64, 0]) and torch.equal(v[P - 3, 0, :2], pv[128:, 0])
+    ring = torch.arange(P - 1, -1, -1, device=DEV, dtype=torch.int32)
+    table = torch.zeros(2, 2, device=DEV, dtype=torch.int32)
+    lens, free, cu, slots, pos = bsa.page_tables(i32([0, 0]), i32([70, 3]), table, ring,
+                                                 i32([2, P - 2]), page, 80)
+    assert table.tolist()[0] == [P - 3, P - 4] and slots[69] == (P - 4) * 64 + 5
+    for dtype, T in ((BF16, 1), (BF16, 30)):  # few rows; 128-row tiles
+        q = torch.randn(T, 8, d, device=DEV).to(dtype)
+        o, _ = bsa.prefix_attn(q, k, v, torch.zeros(T, 0, device=DEV, dtype=torch.int32),
+                               torch.zeros(T, device=DEV, dtype=torch.int32), ids, 130)
+        x = torch.einsum("thd,nd->thn", q.double(), pk[:, 0].double()) / d ** 0.5
+        p = torch.softmax(x, -1)
+        want, W = (torch.einsum("thn,nd->thd", p, y.double()) for y in (pv[:, 0], pv[:, 0].abs()))
+        assert ((o.double() - want).abs() <= 2.0 ** -8 * (1.01 * W + want.abs())
+                + 2.0 ** -14 * W).all()
 
 
 def test_two_streams_at_once():

@@ -859,16 +859,25 @@ def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q
     dev = _device_index(q)
     if o is None:
         o = torch.empty_like(q)  # contiguous: q is, up to the distance of its tokens
+    elif o.shape != shape or o.dtype is not dtype:
+        raise ValueError("o must be like q")
+    else:
+        _on_device(dev, o)
     if lse is None:
         lse = q.new_empty((T, Hq), dtype=torch.float32)
-    if o.shape != shape or o.dtype is not dtype or lse.numel() != T * Hq \
-            or lse.dtype is not torch.float32:
-        raise ValueError("o must be like q, lse [T, Hq] float32")
+    elif lse.numel() != T * Hq or lse.dtype is not torch.float32:
+        raise ValueError("lse must be [T, Hq] float32")
+    else:
+        _on_device(dev, lse)
     table_ld = table_shape[1]
     if ws is None:
         ws = q.new_empty(_prefix_attn_bytes(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len,
                                             max_q), dtype=torch.uint8)
-    _on_device(dev, k_pages, v_pages, table, lens, prefix_table, cu_q, o, lse, ws, status)
+    elif ws.dtype is not torch.uint8:
+        raise ValueError("ws must be uint8")
+    else:
+        _on_device(dev, ws)
+    _on_device(dev, k_pages, v_pages, table, lens, prefix_table, cu_q, status)
     _ints(table, lens, prefix_table, cu_q, status)
     _call(lib().bsa_prefix_attn, dev, "bsa_prefix_attn", q.data_ptr(), q_stride,
           k_pages.data_ptr(), v_pages.data_ptr(), dt, T, B, Hq, Hk, d, page, P, table.data_ptr(),

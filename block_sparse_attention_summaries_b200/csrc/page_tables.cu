@@ -11,16 +11,20 @@
 // G_b - grow_b .. G_b - 1 behind head.  A shrinking request's pages go to the ring's end in request
 // order.  Token t of the packed new tokens belongs to the request whose range of the exclusive sum
 // of new tokens holds it, found by a binary search in shared memory unless the 128 tokens of a warp
-// step all belong to the request before; a page that moves finds its request the same way.  All integer work on a few KB:
-// what bounds it is latency (the lengths' load, a block scan, the dependent page-id load), so it is
-// ONE launch: a cluster of up to 8 CTAs, each of which scans all requests for itself (one load and
-// a scan are cheaper than a second launch or a grid-wide exchange) and then handles its share of
-// the requests' pages and of the tokens.  The cluster barrier between reading lens / free and
-// writing lens_out / free_out lets the caller pass the same arrays (a state advanced in place).
+// step all belong to the request before; a page that moves finds its request the same way.  All
+// integer work on a few KB: what bounds it is latency (the lengths' load, a block scan, the
+// dependent page-id load), so it is ONE launch: a cluster of up to 8 CTAs, each of which scans all
+// requests for itself (one load and a scan are cheaper than a second launch or a grid-wide
+// exchange) and then handles its share of the requests' pages and of the tokens.  The cluster
+// barrier between reading lens / free and writing lens_out / free_out lets the caller pass the same
+// arrays (a state advanced in place). Measured: 5.2 us for a tick of 64 requests, of which 4 are
+// the launch and two dependent loads; 20 us for 1024 requests with a quarter million new tokens
+// (2.3 MB), whose instructions 8 SMs issue.
 //
 // paged_append_kernel.  A copy bound by HBM: one 16-byte chunk of K and of V per thread and step,
 // neighbouring threads on neighbouring chunks of a head's row (256 B at d = 128 bf16), so reads
 // and writes are whole 32-byte sectors whatever the slots' order.
+// Measured: 16,384 tokens of 8 x 128 bf16 (134 MB) in 23.3 us, 5.8 TB/s; 64 tokens in 1.9 us.
 #include <cooperative_groups.h>
 
 #include "bsa_common.cuh"
@@ -174,8 +178,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
     p.cu_new[b] = s_cu[b];
     p.lens_out[b] = s_new[b];
   }
-  // the last entry of s[0 .. B) that is at most x (s ascends, s[0] = 0): of the requests whose ranges
-  // start there, the last is the one that has any
+  // the last entry of s[0 .. B) that is at most x (s ascends, s[0] = 0): of the requests whose
+  // ranges start there, the last is the one that has any
   auto owner = [&](const int* s, int lo, int x) {
     int hi = p.B;
     while (hi - lo > 1) {
@@ -197,8 +201,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
         p.table[(size_t)b * p.ld + pages_of(s_new[b]) + (i - s_drop[b])];
   }
 
-  // slots and positions of the new tokens: a run of consecutive tokens per warp, 128 at a time, four
-  // a lane (with one a lane the 8 SMs spent 14 us issuing the instructions of a quarter million)
+  // slots and positions of the new tokens: a run of consecutive tokens per warp, 128 at a time,
+  // four a lane (with one a lane the 8 SMs spent 14 us issuing the instructions of a quarter
+  // million)
   const int gwarp = rank * warps + warp, gwarps = ranks * warps;
   const int total = s_cu[p.B];
   const long long run = (((long long)p.max_tokens + gwarps - 1) / gwarps + 127) / 128 * 128;

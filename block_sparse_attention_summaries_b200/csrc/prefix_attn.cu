@@ -8,18 +8,21 @@
 // (log2 units), so the prefix is attended once for the rows of ALL requests -- packed, token after
 // token, into full query tiles, whose keys are then read once per tile and not once per request --
 // and each request's own keys only for its own rows.  Both parts may be cut into pieces along the
-// keys when there are too few tiles to fill the GPU; prefix_merge_kernel joins a row's pieces.
+// keys when there are too few tiles to fill the GPU; prefix_merge_kernel joins a row's
+// pieces: bound by L2 (2048 rows of 19 pieces, 20 MB, in 5.6 us) and by latency in small calls, so
+// a warp loads eight pieces of its row at a time.
 //
-// prefix_simt_kernel: float32, CUDA cores (its tensor-core formats would round q, k and the weights).
-// A CTA of 128 threads takes RG rows (of one kv head, row = token * G + head of the group) and a
-// piece of the keys in tiles of 64 (d = 64) or 32: S = Q K^T in registers from shared memory, online
-// softmax with the running maximum of each row in registers of the 8 threads that share it, P through
-// shared memory, O += P V in registers.  A warp is 4 x 8 threads of 4 rows and 8 keys each (RG = 64,
-// d = 64), so that its reads of Q and of K are one shared-memory wavefront each: with 2 x 16 threads of
-// 4 x 4 the wavefronts (79 % of their peak) held the FMAs at 50 % (159 requests behind 46K keys: 1.10
-// ms).  The next tile is copied (cp.async) while one is
-// worked on, its page ids read a tile earlier still: with loads in line a tile took 5 us, the time of
-// two dependent trips to memory.
+// prefix_simt_kernel: float32, CUDA cores (its tensor-core formats would round q, k and the
+// weights). A CTA of 128 threads takes RG rows (of one kv head, row = token * G + head of the
+// group) and a piece of the keys in tiles of 64 (d = 64) or 32: S = Q K^T in registers from shared
+// memory, online softmax with the running maximum of each row in registers of the 8 threads that
+// share it, P through shared memory, O += P V in registers.  A warp is 4 x 8 threads of 4 rows and
+// 8 keys each (RG = 64, d = 64), so that its reads of Q and of K are one shared-memory wavefront
+// each: with 2 x 16 threads of 4 x 4 the wavefronts (79 % of their peak) held the FMAs at 50 % (159
+// requests of 16 single-key heads behind 46K keys, d = 64: 1.10 ms; now 1.01 ms, 30 TFLOP/s of the
+// CUDA cores' 72).  The next tile is copied (cp.async) while one is worked on, its page ids read a
+// tile earlier still: with loads in line a tile took 5 us, the time of two dependent trips to
+// memory.
 #include "prefix_attn.cuh"
 
 namespace bsa {
@@ -288,8 +291,9 @@ __global__ void __launch_bounds__(kPsThreads, 2) prefix_simt_kernel(const Prefix
     u /= p.ns2;
     un.h = u / g.tiles2;
     u %= g.tiles2;
-    constexpr int kShift = RG2 == 64 ? 6 : 4;
-    const int2 place = pa_place(p, u, kShift);
+    // 16-row tiles are taken when no request has more than 16 rows: one each
+    int2 place = make_int2(u, 0);
+    if constexpr (RG2 == 64) place = pa_place(p, u, 6);
     const int tile = place.y, b = max(place.x, 0);
     if (place.x < 0 || tile < 0) return;
     const PaRequest r = pa_request(p, b);
@@ -327,8 +331,8 @@ constexpr int kRowsCtas = 2 * kSMs;  // of the few-rows kernel: two per SM
 constexpr int kRowsMax = 64;         // its rows
 constexpr int kClusterCtas = 16;     // of a kv head in a small call
 constexpr long long kClusterTiles = 4 * kClusterCtas;  // key tiles of a kv head up to which one is small
-// Key tiles of 32 KB (over all heads and row groups) up to which the few-rows kernel takes the prefix of
-// more rows: four a CTA.
+// Key tiles of 32 KB (over all heads and row groups) up to which the few-rows kernel takes the
+// prefix of more rows: four a CTA.
 constexpr long long kPrefixTiles = 4 * kRowsCtas;
 
 // Which kernel does which part.
@@ -363,8 +367,8 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
   } else if (dt == BSA_BF16) {
     // Up to 64 rows share an own key: the few-rows kernel.  It takes the prefix too where all rows
     // of a kv head fit its tile, or where reading the prefix once per row group is cheap; else the
-    // rows of all requests fill 128-row tiles (32 rows of d = 64 behind 64K keys: 80 us there, 87 us
-    // with 32-row tiles here, whose warps wait for one another more than for HBM).
+    // rows of all requests fill 128-row tiles (32 rows of d = 64 behind 64K keys: 80 us there, 87
+    // us with 32-row tiles here, whose warps wait for one another more than for HBM).
     w.mt = mt_of(rows_q);
     const int groups = prefix_len ? tiles(rows, 16 * w.mt) : 0;
     if (groups <= 1 || (long long)groups * Hk * tiles(prefix_len, 8192 / d) <= kPrefixTiles)
@@ -374,8 +378,8 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
     w.prefix_rows = 16 * w.mt;
     w.own_rows = (int)rows_q;
     w.items = ((long long)w.groups + B) * Hk;
-    // A small call is one launch: a cluster per kv head (4 requests behind 1000 tokens: 11.5 us as two).
-    // With fewer CTAs than the GPU holds it loses that again once each has several tiles.
+    // A small call is one launch: a cluster per kv head (4 requests behind 1000 tokens: 11.5 us as
+    // two). With fewer CTAs than the GPU holds it loses that again once each has several tiles.
     w.cluster = !w.tc1 && (long long)w.groups * tiles(prefix_len, 8192 / d) +
                                   (long long)B * tiles(keys2, 8192 / d) <= kClusterTiles;
     w.item_ctas = w.cluster ? kClusterCtas : kRowsCtas;
@@ -383,7 +387,7 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
     w.rg2 = rows_q <= 16 ? 16 : 64;
     w.rg1 = w.rg2 == 64 || rows > 32 ? 64 : rows > 16 ? 32 : 16;
     w.simt1 = prefix_len ? tiles(rows, w.rg1) : 0;
-    w.simt2 = keys2 ? (int)pa_places(T, B, G, w.rg2 == 64 ? 6 : 4) : 0;
+    w.simt2 = keys2 ? (w.rg2 == 64 ? (int)pa_places(T, B, G, 6) : B) : 0;
   }
   if (w.tc1) w.ns1 = pieces_for((long long)w.tc1 * Hk, kSMs, (prefix_len + 127) / 128, 4);
   // Two CTAs per SM: half for the prefix, unless the own keys fill the GPU by themselves.
@@ -420,8 +424,7 @@ bsa_status launch_simt(const PrefixParams& p, const PrefixPlan& w, cudaStream_t 
   static std::atomic<unsigned long long> done{0};
   if (!allow_smem(prefix_simt_kernel<D, RG1, RG2>, smem, done) ||
       !launch_pdl(prefix_simt_kernel<D, RG1, RG2>, (int)(units1 + units2), 1, kPsThreads, smem, st,
-                  p,
-                  SimtGrid{(int)units1, w.simt2}))
+                  p, SimtGrid{(int)units1, w.simt2}))
     return BSA_ERR_CUDA;
   return BSA_OK;
 }

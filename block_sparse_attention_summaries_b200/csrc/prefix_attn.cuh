@@ -30,9 +30,9 @@ struct PrefixParams {
   float* part_o;
   float2* part_ml;
   int ns1, ns2;
-  // Pieces of prefix_attn_rows: an item is a kv head and a group of packed rows (prefix) or a request
-  // (own keys); *_cta[item] = first and last CTA that worked on it, and CTA c's piece of it is a run
-  // of prefix_rows / own_rows rows of item_o [row][d] and item_ml [row] (pa_piece_row).
+  // Pieces of prefix_attn_rows: an item is a kv head and a group of packed rows (prefix) or a
+  // request (own keys); *_cta[item] = first and last CTA that worked on it, and CTA c's piece of it
+  // is a run of prefix_rows / own_rows rows of item_o [row][d] and item_ml [row] (pa_piece_row).
   int groups;       // row groups of the prefix, 0: the prefix is not among the items
   int2* item_cta;   // [Hk * groups] prefix items, then [B * Hk] own ones
   float* item_o;
@@ -67,9 +67,9 @@ __device__ __forceinline__ int2* pa_item_cta(const PrefixParams& p, bool prefix,
   return p.item_cta + (prefix ? (size_t)h * p.groups + i
                               : (size_t)p.Hk * p.groups + (size_t)i * p.Hk + h);
 }
-// First row of CTA c's piece of an item: kv head h, group or request i.  CTAs and items both only grow
-// along the order in which the items' tiles are dealt out, so item + CTA is a place of its own; with a
-// cluster per head, the order is within the head.
+// First row of CTA c's piece of an item: kv head h, group or request i.  CTAs and items both only
+// grow along the order in which the items' tiles are dealt out, so item + CTA is a place of its
+// own; with a cluster per head, the order is within the head.
 __device__ __forceinline__ long long pa_piece_row(const PrefixParams& p, bool prefix, int h, int i,
                                                   int c) {
   const long long before =  // pieces of the prefix
@@ -83,9 +83,9 @@ __device__ __forceinline__ long long pa_piece_row(const PrefixParams& p, bool pr
          (p.cluster ? (long long)h * (p.B + p.item_ctas) + i : (long long)i * p.Hk + h) *
              p.own_rows + (long long)c * p.own_rows;
 }
-// Row tiles of the requests, 1 << shift rows each, as places in a row: request b's start at (its first
-// packed row >> shift) + b, which leaves room for a last, partly filled one each, so (T * G >> shift) +
-// B places hold them all however the tokens are spread.
+// Row tiles of the requests, 1 << shift rows each, as places in a row: request b's start at (its
+// first packed row >> shift) + b, which leaves room for a last, partly filled one each, so (T * G
+// >> shift) + B places hold them all however the tokens are spread.
 inline long long pa_places(int T, int B, int G, int shift) {
   return ((long long)T * G >> shift) + B;
 }
@@ -244,8 +244,8 @@ bool launch_pdl(void (*kern)(Args...), int grid, int cluster, int threads, int s
   return false;
 }
 
-// Dynamic shared memory above 48 KB and clusters above 8 CTAs, asked for once per device (`done`: one
-// bit each).
+// Dynamic shared memory above 48 KB and clusters above 8 CTAs, asked for once per device (`done`:
+// one bit each).
 template <typename Kern>
 bool allow_smem(Kern kern, int bytes, std::atomic<unsigned long long>& done,
                 bool large_cluster = false) {

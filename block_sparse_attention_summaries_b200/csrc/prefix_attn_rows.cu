@@ -4,12 +4,13 @@
 // fits.
 //
 // An item is (request, kv head) -- or (prefix, kv head, group of packed rows) -- and its keys in
-// tiles of 64 (d = 128) or 128 (d = 64).  The tiles of all items, one after another, are cut into equal runs, one per CTA (two
-// CTAs per SM), whatever the requests' lengths: a CTA's producer warp walks its run without stopping
-// at item borders, so the ring of tiles stays full while the consumers change rows.  An item is then
-// cut into at most the pieces that its CTAs saw; piece (item, CTA) is stored at slot item + CTA,
-// unique because both only grow along the run, and the merge kernel joins an item's slots.  In a small
-// call a cluster of CTAs does this per kv head and joins the pieces itself behind a cluster barrier.
+// tiles of 64 (d = 128) or 128 (d = 64).  The tiles of all items, one after another, are cut into
+// equal runs, one per CTA (two CTAs per SM), whatever the requests' lengths: a CTA's producer warp
+// walks its run without stopping at item borders, so the ring of tiles stays full while the
+// consumers change rows.  An item is then cut into at most the pieces that its CTAs saw; piece
+// (item, CTA) is stored at slot item + CTA, unique because both only grow along the run, and the
+// merge kernel joins an item's slots.  In a small call a cluster of CTAs does this per kv head and
+// joins the pieces itself behind a cluster barrier.
 //   warps 0-3: per tile, S of 16 or 32 keys each for MT tiles of 16 rows (mma.sync m16n8k16: an M = 128
 //              tcgen05 tile would be padding for half its rows or more, and HBM bounds the rate far
 //              below either); the row maxima meet in shared memory, each warp exponentiates its
@@ -21,6 +22,8 @@
 //              wait for memory (items of one tile took 5 us each before, 64 x 64 tokens x 8 heads
 //              15.8 us in all, now 11.2 us)
 // V rows without a key are masked to zero in the registers that feed the products.
+// Measured at 32 / 8 heads, d = 128: 512 requests of 1024 own tokens (2.15 GB) in 343 us, 6.3 TB/s;
+// 64 of up to 1024 (144 MB) in 26 us.
 #include <cooperative_groups.h>
 
 #include "prefix_attn.cuh"
@@ -33,8 +36,8 @@ constexpr float kRRescale = 8.f;  // log2 units: O is rescaled when a row's maxi
 
 template <int D, int MT>
 struct RowsSmem {
-  // keys of a tile: 32 KB of K and V; the barriers and shuffles of a tile cost the same at d = 64 as
-  // at d = 128 (64-key tiles at d = 64: 117 us where this takes 70)
+  // keys of a tile: 32 KB of K and V; the barriers and shuffles of a tile cost the same at d = 64
+  // as at d = 128 (64-key tiles at d = 64: 117 us where this takes 70)
   static constexpr int kKeys = 8192 / D;
   static constexpr int kHalf = kKeys * 128;       // rows x 128 B, 128-byte swizzle
   static constexpr int kTile = (D / 64) * kHalf;  // K or V
@@ -93,8 +96,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// Adds the infinities and NaNs of V at own keys [j0, n), D / 4 columns from col, to the rows that see
-// them: a warp, which has written those columns.  Not inline: it runs for bad values only.
+// Adds the infinities and NaNs of V at own keys [j0, n), D / 4 columns from col, to the rows that
+// see them: a warp, which has written those columns.  Not inline: it runs for bad values only.
 template <int D>
 __device__ __noinline__ void add_cleaned(const __nv_bfloat16* v, const int* pages, int num_pages,
                                          int page_shift, int Hk, int h, int j0, int n,
@@ -187,8 +190,8 @@ __global__ void __launch_bounds__(kRThreads, 2)
     // nothing to attend
   } else if (warp == 4) {
     // ------------------------------------------------------------------------- producer
-    // where the run is: request (-1: the prefix), head of the run's (prefix: head * groups + group),
-    // tile of the item
+    // where the run is: request (-1: the prefix), head of the run's (prefix: head * groups +
+    // group), tile of the item
     struct Place {
       int b, h, tile, tiles, n, t0, nrows, first_pos;
     } c;

@@ -13,13 +13,13 @@
 // of new tokens holds it, found by a binary search in shared memory unless the 128 tokens of a warp
 // step all belong to the request before; a page that moves finds its request the same way.  All
 // integer work on a few KB: what bounds it is latency (the lengths' load, a block scan, the
-// dependent page-id load), so it is ONE launch: a cluster of up to 8 CTAs, each of which scans all
+// dependent page-id load), so it is ONE launch: a cluster of up to 16 CTAs, each of which scans all
 // requests for itself (one load and a scan are cheaper than a second launch or a grid-wide
 // exchange) and then handles its share of the requests' pages and of the tokens.  The cluster
 // barrier between reading lens / free and writing lens_out / free_out lets the caller pass the same
 // arrays (a state advanced in place). Measured: 5.2 us for a tick of 64 requests, of which 4 are
-// the launch and two dependent loads; 20 us for 1024 requests with a quarter million new tokens
-// (2.3 MB), whose instructions 8 SMs issue.
+// the launch and two dependent loads; 14 us for 1024 requests with a quarter million new tokens
+// (2.3 MB), whose instructions 8 to 16 SMs issue.
 //
 // paged_append_kernel.  A copy bound by HBM: one 16-byte chunk of K and of V per thread and step,
 // neighbouring threads on neighbouring chunks of a head's row (256 B at d = 128 bf16), so reads
@@ -28,6 +28,7 @@
 #include <cooperative_groups.h>
 
 #include "bsa_common.cuh"
+#include "launch.cuh"
 
 namespace bsa {
 namespace {
@@ -36,7 +37,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kPtThreads = 1024;
 constexpr int kPtMaxB = 8192;      // requests of a step (shared memory: five ints each)
-constexpr int kPtCluster = 8;      // portable cluster size
+constexpr int kPtCluster = 16;     // CTAs of a large step
 // Up to this many requests + new tokens one CTA does it all: above, its 1024 threads would take
 // more than a few rounds.
 constexpr int kPtOneCta = 4096;
@@ -348,16 +349,14 @@ extern "C" bsa_status bsa_page_tables(int B, int page, const int* lens, const in
                         lens,     new_lens, table,    ring,      free_in,    lens_out,
                         free_out, cu_new,   slots,    positions, status};
   const int smem = (5 * B + 1) * (int)sizeof(int);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-          cudaSuccess) {
-    (void)cudaGetLastError();
+  static std::atomic<unsigned long long> done{0};
+  if (!allow_smem(page_tables_kernel, (5 * kPtMaxB + 1) * (int)sizeof(int), done, true))
     return BSA_ERR_CUDA;
-  }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   const long long work = (long long)B + max_tokens;
-  const unsigned ctas = work <= kPtOneCta ? 1u : (unsigned)kPtCluster;
+  // 16 CTAs want to be two to an SM: with 8 a quarter million tokens took 20 us, with 16 14 us
+  const unsigned ctas = work <= kPtOneCta ? 1u : smem <= 100 * 1024 ? kPtCluster : kPtCluster / 2;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;

@@ -2,8 +2,7 @@
 // partial results that the merge kernel joins.
 #pragma once
 
-#include <atomic>
-
+#include "launch.cuh"
 #include "tc_common.cuh"
 
 namespace bsa {
@@ -242,26 +241,6 @@ bool launch_pdl(void (*kern)(Args...), int grid, int cluster, int threads, int s
   if (cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess) return true;
   (void)cudaGetLastError();
   return false;
-}
-
-// Dynamic shared memory above 48 KB and clusters above 8 CTAs, asked for once per device (`done`:
-// one bit each).
-template <typename Kern>
-bool allow_smem(Kern kern, int bytes, std::atomic<unsigned long long>& done,
-                bool large_cluster = false) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (bit && (done.load(std::memory_order_relaxed) & bit)) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
-          cudaSuccess ||
-      (large_cluster && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                                             1) != cudaSuccess)) {
-    (void)cudaGetLastError();
-    return false;
-  }
-  done.fetch_or(bit, std::memory_order_relaxed);
-  return true;
 }
 
 // prefix_attn_tc.cu

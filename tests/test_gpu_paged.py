@@ -431,6 +431,14 @@ def test_page_tables(B, page, in_place):
     check_tables(lens, new, table, ring, free, page, total + 5, off=77, in_place=in_place)
 
 
+@pytest.mark.parametrize("B", [5000, 8192])
+def test_page_tables_most_requests(B):
+    rng = np.random.default_rng(B)
+    lens, table, ring, free = make_tables(rng, B, 16, 3, 2 * B)
+    new = rng.integers(0, 49, B).astype(np.int32)
+    check_tables(lens, new, table, ring, free, 16, int(np.maximum(new - lens, 0).sum()) + 3)
+
+
 @pytest.mark.parametrize("spare", [0, 1, 3, 10])
 def test_page_tables_exhausted(spare):
     rng = np.random.default_rng(spare)

@@ -357,21 +357,30 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
   const long long keys2 = (long long)table_ld * page;
   auto tiles = [](long long n, int of) { return (int)((n + of - 1) / of); };  // of a length
   auto mt_of = [](long long n) { return n <= 16 ? 1 : n <= 32 ? 2 : 4; };
-  if (dt == BSA_BF16 && rows_q > kRowsMax) {
-    // A request with more than 64 rows: 128-row tiles on the tensor cores.  Requests that fill half
-    // a tile on average keep their rows to themselves: prefix and own keys in one pass.  Below that
-    // the padding would cost more than the merge.
+  // 33 to 64 rows a request: its own tensor-core tile costs about 6 us to start and 1 us per 128
+  // keys, on 148 SMs; the few-rows kernel 5 us per 32 KB tile, on 296 CTAs (64 requests of 1000 keys
+  // and 56 rows: 108 against 131 us; 142 of 13 keys and 36 rows: 105 against 59 us).
+  const long long own = (long long)B * Hk;
+  const bool few = rows_q <= 32 || (rows_q <= kRowsMax &&
+                                    5 * ((own * tiles(keys2, 8192 / d) + kRowsCtas - 1) /
+                                         kRowsCtas) <=
+                                        (own + kSMs - 1) / kSMs * (6 + tiles(keys2, 128)));
+  if (dt == BSA_BF16 && !few) {
+    // More: 128-row tiles on the tensor cores.  Requests that fill half a tile on average keep
+    // their rows to themselves: prefix and own keys in one pass.  Below that the padding would cost
+    // more than the merge.
     w.fused = rows >= 64LL * B;
     w.tc2 = (int)pa_places(T, B, G, 8);
     if (!w.fused && prefix_len) w.tc1 = tiles(rows, 256);
   } else if (dt == BSA_BF16) {
-    // Up to 64 rows share an own key: the few-rows kernel.  It takes the prefix too where all rows
-    // of a kv head fit its tile, or where reading the prefix once per row group is cheap; else the
-    // rows of all requests fill 128-row tiles (32 rows of d = 64 behind 64K keys: 80 us there, 87
-    // us with 32-row tiles here, whose warps wait for one another more than for HBM).
+    // The few-rows kernel.  It takes the prefix too where all rows of a kv head fit 16, or where
+    // reading the prefix once per row group is cheap; else the rows of all requests fill 128-row
+    // tiles (32 rows of d = 64 behind 64K keys: 80 us there, 87 us with 32-row tiles here, whose
+    // warps wait for one another more than for HBM).
     w.mt = mt_of(rows_q);
     const int groups = prefix_len ? tiles(rows, 16 * w.mt) : 0;
-    if (groups <= 1 || (long long)groups * Hk * tiles(prefix_len, 8192 / d) <= kPrefixTiles)
+    if ((groups <= 1 && w.mt == 1) ||
+        (long long)groups * Hk * tiles(prefix_len, 8192 / d) <= kPrefixTiles)
       w.groups = groups;
     else
       w.tc1 = tiles(rows, 256);

@@ -23,12 +23,15 @@
 // CUDA cores' 72).  The next tile is copied (cp.async) while one is worked on, its page ids read a
 // tile earlier still: with loads in line a tile took 5 us, the time of two dependent trips to
 // memory.
+#include <cooperative_groups.h>
+
 #include "prefix_attn.cuh"
 
 namespace bsa {
 namespace {
 
 constexpr int kPsThreads = 128;
+constexpr int kClusterCtas = 16;  // of a kv head in a small call
 
 template <int D, int RG>
 struct SimtSmem {
@@ -43,8 +46,8 @@ struct SimtSmem {
 };
 
 struct SimtGrid {
-  int units1;  // CTAs of the prefix: tiles of packed rows x kv heads x pieces
-  int tiles2;  // places of request tiles (pa_place)
+  int tiles1;  // tiles of the packed rows
+  int tiles2;  // of the requests: one each, or places (pa_place)
 };
 
 // The rows and keys of a CTA.
@@ -264,20 +267,16 @@ __device__ __forceinline__ void simt_unit(const PrefixParams& p, const SimtUnit&
   }
 }
 
-// RG1 rows a tile of the packed rows against the prefix, RG2 of a request against its own keys
+// Unit u of kv head h: the packed rows' tiles x pieces (RG1 rows each) against the prefix, then the
+// requests' (RG2 rows) against their own keys.
 template <int D, int RG1, int RG2>
-__global__ void __launch_bounds__(kPsThreads, 2) prefix_simt_kernel(const PrefixParams p,
-                                                                 const SimtGrid g) {
-  extern __shared__ __align__(16) float smf[];
-  pdl_wait();
-  pdl_trigger();
+__device__ __forceinline__ void simt_unit_of(const PrefixParams& p, const SimtGrid& g, int h, int u,
+                                             float* smf) {
   SimtUnit un;
-  int u = blockIdx.x;
-  if (u < g.units1) {
+  un.h = h;
+  if (u < g.tiles1 * p.ns1) {
     un.piece = u % p.ns1;
-    u /= p.ns1;
-    un.h = u % p.Hk;
-    un.r0 = u / p.Hk * RG1;
+    un.r0 = u / p.ns1 * RG1;
     un.nrows = min(RG1, pa_tokens(p) * p.G - un.r0);
     un.pages = p.ptable;
     un.n = p.prefix_len;
@@ -286,11 +285,9 @@ __global__ void __launch_bounds__(kPsThreads, 2) prefix_simt_kernel(const Prefix
     un.pieces = p.ns1;
     simt_unit<D, RG1>(p, un, smf);
   } else {
-    u -= g.units1;
+    u -= g.tiles1 * p.ns1;
     un.piece = u % p.ns2;
     u /= p.ns2;
-    un.h = u / g.tiles2;
-    u %= g.tiles2;
     // 16-row tiles are taken when no request has more than 16 rows: one each
     int2 place = make_int2(u, 0);
     if constexpr (RG2 == 64) place = pa_place(p, u, 6);
@@ -307,6 +304,41 @@ __global__ void __launch_bounds__(kPsThreads, 2) prefix_simt_kernel(const Prefix
     un.pieces = p.ns2;
     simt_unit<D, RG2>(p, un, smf);
   }
+}
+
+// A unit per CTA; or, in a small call, a cluster of CTAs per kv head, which takes its units in turn and
+// joins their pieces behind a cluster barrier.
+template <int D, int RG1, int RG2>
+__global__ void __launch_bounds__(kPsThreads, 2) prefix_simt_kernel(const PrefixParams p,
+                                                                    const SimtGrid g) {
+  extern __shared__ __align__(16) float smf[];
+  pdl_wait();
+  pdl_trigger();
+  const int units1 = g.tiles1 * p.ns1, units2 = g.tiles2 * p.ns2;  // of a head
+  if (!p.cluster) {
+    // the prefix's units, longer as a rule, of all heads first
+    int i = blockIdx.x, h;
+    if (i < units1 * p.Hk) {
+      h = i / units1;
+      i -= h * units1;
+    } else {
+      i -= units1 * p.Hk;
+      h = i / units2;
+      i += units1 - h * units2;
+    }
+    simt_unit_of<D, RG1, RG2>(p, g, h, i, smf);
+    return;
+  }
+  const int h = blockIdx.x / kClusterCtas, me = blockIdx.x % kClusterCtas;
+  for (int u = me; u < units1 + units2; u += kClusterCtas) {
+    if (u != me) __syncthreads();  // the unit before has been read
+    simt_unit_of<D, RG1, RG2>(p, g, h, u, smf);
+  }
+  cooperative_groups::this_cluster().sync();
+  const int n = pa_tokens(p) << p.g_shift, warp = threadIdx.x >> 5;
+  for (int r = me * (kPsThreads / 32) + warp; r < n; r += kClusterCtas * (kPsThreads / 32))
+    pa_join_row<float, D>(p, r >> p.g_shift, (h << p.g_shift) + (r & (p.G - 1)),
+                          threadIdx.x & 31);
 }
 
 // Joins the pieces of a row, a warp per row.
@@ -329,8 +361,9 @@ int pieces_for(long long units, long long ctas, long long tiles, int least) {
 
 constexpr int kRowsCtas = 2 * kSMs;  // of the few-rows kernel: two per SM
 constexpr int kRowsMax = 64;         // its rows
-constexpr int kClusterCtas = 16;     // of a kv head in a small call
-constexpr long long kClusterTiles = 4 * kClusterCtas;  // key tiles of a kv head up to which one is small
+// Key tiles of a kv head up to which a call is small: of the few-rows kernel, of the CUDA cores (a
+// tile takes those 2 us: with up to 8 a CTA 10 requests of 500 keys took 57 us instead of 45)
+constexpr long long kClusterTiles = 4 * kClusterCtas, kClusterTiles2 = 2 * kClusterCtas;
 // Key tiles of 32 KB (over all heads and row groups) up to which the few-rows kernel takes the
 // prefix of more rows: four a CTA.
 constexpr long long kPrefixTiles = 4 * kRowsCtas;
@@ -341,7 +374,7 @@ struct PrefixPlan {
   int simt1, simt2;        // such tiles, and places of such tiles (pa_place); 0: not its part
   int tc1, tc2;            // 256-row tiles on the tensor cores, the same way
   bool fused, direct;      // request tiles take the prefix too; one piece in all, no merge
-  bool cluster;            // few-rows kernel as one cluster per kv head, which joins the pieces itself
+  bool cluster;            // a cluster per kv head, which joins the pieces itself (one launch)
   int mt, groups;          // few-rows kernel: 16-row tiles (0: not used), row groups of the prefix
   int ns1, ns2, prefix_rows, own_rows, item_ctas;
   long long items;
@@ -399,15 +432,25 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
     w.simt2 = keys2 ? (w.rg2 == 64 ? (int)pa_places(T, B, G, 6) : B) : 0;
   }
   if (w.tc1) w.ns1 = pieces_for((long long)w.tc1 * Hk, kSMs, (prefix_len + 127) / 128, 4);
-  // Two CTAs per SM: half for the prefix, unless the own keys fill the GPU by themselves.
-  if (w.simt1)
-    w.ns1 = pieces_for((long long)w.simt1 * Hk,
-                       (long long)w.simt2 * Hk > 2 * kSMs ? 2 * kSMs : kSMs,
-                       tiles(prefix_len, 4096 / d), 2);
+  if (w.simt1 || w.simt2) {
+    const int t1 = tiles(prefix_len, 4096 / d), t2 = tiles(keys2, 4096 / d);  // of 16 KB
+    const long long all = (long long)w.simt1 * t1 + (long long)w.simt2 * t2;
+    w.cluster = all <= kClusterTiles2;
+    if (w.cluster) {
+      const int len = std::max(2, tiles(all, kClusterCtas));  // key tiles of a piece
+      w.ns1 = w.simt1 ? tiles(t1, len) : 0;
+      w.ns2 = w.simt2 ? tiles(t2, len) : 0;
+    } else {
+      // Two CTAs per SM: half for the prefix, unless the own keys fill the GPU by themselves.
+      const long long own2 = (long long)w.simt2 * Hk;
+      if (w.simt1)
+        w.ns1 = pieces_for((long long)w.simt1 * Hk, own2 > 2 * kSMs ? 2 * kSMs : kSMs, t1, 2);
+      if (w.simt2) w.ns2 = pieces_for(own2, kSMs, t2, 2);
+    }
+  }
   if (w.tc2)
     w.ns2 = pieces_for((rows + 255) / 256 * Hk, kSMs,
                        (keys2 + (w.fused ? prefix_len : 0) + 127) / 128, 4);
-  if (w.simt2) w.ns2 = pieces_for((long long)w.simt2 * Hk, kSMs, tiles(keys2, 4096 / d), 2);
   w.direct = w.tc2 && !w.tc1 && w.ns2 == 1;
   const long long all = w.direct ? 0 : (long long)T * Hq * (w.ns1 + w.ns2);
   w.ml_bytes = align_up((size_t)all * sizeof(float2), 256);
@@ -431,9 +474,11 @@ bsa_status launch_simt(const PrefixParams& p, const PrefixPlan& w, cudaStream_t 
   if (units1 + units2 == 0) return BSA_OK;
   const int smem = std::max(SimtSmem<D, RG1>::kTotal, SimtSmem<D, RG2>::kTotal);
   static std::atomic<unsigned long long> done{0};
-  if (!allow_smem(prefix_simt_kernel<D, RG1, RG2>, smem, done) ||
-      !launch_pdl(prefix_simt_kernel<D, RG1, RG2>, (int)(units1 + units2), 1, kPsThreads, smem, st,
-                  p, SimtGrid{(int)units1, w.simt2}))
+  if (!allow_smem(prefix_simt_kernel<D, RG1, RG2>, smem, done, true) ||
+      !launch_pdl(prefix_simt_kernel<D, RG1, RG2>,
+                  w.cluster ? kClusterCtas * p.Hk : (int)(units1 + units2),
+                  w.cluster ? kClusterCtas : 1, kPsThreads, smem, st, p,
+                  SimtGrid{w.simt1, w.simt2}))
     return BSA_ERR_CUDA;
   return BSA_OK;
 }
@@ -445,14 +490,13 @@ bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status,
     rc = prefix_attn_tc(p, D, w.tc1, w.tc2, w.fused, w.direct, status, st);
     if (rc != BSA_OK || w.direct) return rc;
     if (w.mt) rc = prefix_attn_rows(p, D, w.mt, w.tc1 > 0, status, st);
-    if (rc != BSA_OK || w.cluster) return rc;
   } else {
     rc = w.rg2 == 64   ? launch_simt<D, 64, 64>(p, w, st)
          : w.rg1 == 64 ? launch_simt<D, 64, 16>(p, w, st)
          : w.rg1 == 32 ? launch_simt<D, 32, 16>(p, w, st)
                        : launch_simt<D, 16, 16>(p, w, st);
   }
-  if (rc != BSA_OK) return rc;
+  if (rc != BSA_OK || w.cluster) return rc;
   const long long rows = (long long)p.T * p.Hq;
   return launch_pdl(prefix_merge_kernel<T, D>, (int)((rows + 7) / 8), 1, 256, 0, st, p)
              ? BSA_OK

@@ -300,9 +300,10 @@ def test_tokens_before_the_first_request_are_left(dtype, nq):
 
 @pytest.mark.parametrize("B,n,ld", [(1, 1, 1), (2, 17, 2), (9, 40, 3), (30, 64, 4), (60, 16, 1)])
 @pytest.mark.parametrize("heads,kv_heads,d", [(8, 8, 64), (32, 8, 128), (8, 1, 128)])
-def test_small_calls(B, n, ld, heads, kv_heads, d):
-    """Small enough for one launch, up to and past the border; again with the lengths grown."""
-    m = Batch(15, BF16, heads, kv_heads, d, 16, 100, [1] * B, [1 + (n + i) % n for i in range(B)],
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_small_calls(dtype, B, n, ld, heads, kv_heads, d):
+    """Small enough for one launch, up to and past the border; twice."""
+    m = Batch(15, dtype, heads, kv_heads, d, 16, 100, [1] * B, [1 + (n + i) % n for i in range(B)],
               decode=True, spare_ld=ld)
     for _ in range(2):
         m.check(*m.run())
@@ -402,11 +403,12 @@ def make_tables(rng, B, page, ld, spare):
     return lens.astype(np.int32), table, ring, np.array([head, spare], np.int32)
 
 
-def check_tables(lens, new, table, ring, free, page, max_tokens, off=0, in_place=False):
+def check_tables(lens, new, table, ring, free, page, max_tokens, off=0, in_place=False,
+                 into_new=False):
     want = plain_tables(lens, new, table, ring, free, page, max_tokens, off)
     g = [i32(x) for x in (lens, new, table, ring, free)]
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
-    kw = dict(lens_out=g[0], free_out=g[4]) if in_place else {}
+    kw = dict(lens_out=g[1] if into_new else g[0], free_out=g[4]) if in_place else {}
     got = bsa.page_tables(*g, page, max_tokens, pos_offset=off, status=status, **kw)
     got = [x.cpu().numpy().tolist() for x in got]
     for a, b, name in zip(got, want, ["lens", "free", "cu", "slots", "positions"]):
@@ -466,6 +468,24 @@ def test_page_tables_bad_states():
     full = np.array([5, len(ring)], np.int32)
     want = check_tables(lens, np.zeros_like(new), table, ring, full, 16, 10)
     assert want[7] & 4
+
+
+@pytest.mark.parametrize("B", [3, 1500])
+def test_page_tables_into_the_new_lengths(B):
+    """lens_out = new_lens; the refused requests read their old length there."""
+    rng = np.random.default_rng(B)
+    lens, table, ring, free = make_tables(rng, B, 32, 4, B // 2)
+    new = rng.integers(0, 129, B).astype(np.int32)
+    new[B // 2] = 1000
+    check_tables(lens, new, table, ring, free, 32, 5000, in_place=True, into_new=True)
+
+
+def test_page_tables_without_tokens():
+    """No places for tokens: the tables still move."""
+    rng = np.random.default_rng(1)
+    lens, table, ring, free = make_tables(rng, 9, 16, 3, 20)
+    new = np.minimum(lens + 3, 48).astype(np.int32)
+    assert check_tables(lens, new, table, ring, free, 16, 0)[7] == 8
 
 
 def test_page_tables_no_requests():
@@ -571,6 +591,8 @@ class Server:
         W = torch.einsum("ikgj,jkd->ikgd", p, v.abs()).reshape(nq, self.heads, d)
         # bf16 weights and output (2^-8 each) beside float32 sums (under 2^-14 here: |s| < 2^4,
         # a few hundred terms)
+        if self.dtype == F32:
+            return o, 2.0 ** -14 * W
         return o, 2.0 ** -8 * (1.01 * W + o.abs()) + 2.0 ** -14 * W
 
 
@@ -603,8 +625,9 @@ SCRIPT = ([{0: 37, 1: 1, 2: 16, 3: 50}] + [{b: 1 for b in range(4)}] * 3 +
           [{1: None, 2: None}, {0: 20, 5: 33, 3: 1}] + [{0: 1, 3: 1, 4: 1, 5: 1}] * 4)
 
 
-def test_serving_steps():
-    s = Server()
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_serving_steps(dtype):
+    s = Server(dtype=dtype)
     run_script(s, SCRIPT, s.step)
 
 

@@ -218,7 +218,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
   for (int w0 = (int)min((long long)p.max_tokens, gwarp * run); w0 < t_end; w0 += 128) {
     const int t0 = w0 + 4 * lane;
     int slot[4] = {-1, -1, -1, -1}, pos[4] = {-1, -1, -1, -1};
-    if (w0 + 128 <= s_cu[lo + 1]) {  // all in the request of the tokens before
+    if (w0 >= total) {
+      // no tokens (nor, without requests, an s_cu[1])
+    } else if (w0 + 128 <= s_cu[lo + 1]) {  // all in the request of the tokens before
       const int len = s_len[lo];
       if (len >= 0) {
         const int own = len + (t0 - s_cu[lo]);
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
           pos[e] = own + e + p.pos_offset;
         }
       }
-    } else if (w0 < total) {
+    } else {
       int b = owner(s_cu, lo, min(t0, total - 1));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

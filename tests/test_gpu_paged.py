@@ -495,6 +495,20 @@ def test_page_tables_no_requests():
     assert free.tolist() == [1, 2] and cu.tolist() == [0] and slots.tolist() == [-1] * 5
 
 
+@pytest.mark.parametrize("max_tokens", [128, 1000, 300000])
+def test_page_tables_no_requests_many_places(max_tokens):
+    """Places for whole warps of tokens, after a step whose sums are still in shared memory."""
+    rng = np.random.default_rng(2)
+    lens, table, ring, free = make_tables(rng, 300, 16, 40, 20000)
+    new = (lens + 300).astype(np.int32)
+    check_tables(lens, new, table, ring, free, 16, 300 * 300)
+    e = torch.empty(0, dtype=torch.int32, device=DEV)
+    _, free, cu, slots, pos = bsa.page_tables(e, e, e.view(0, 4), i32([1, 2, 0]), i32([1, 2]), 16,
+                                              max_tokens)
+    assert free.tolist() == [1, 2] and cu.tolist() == [0]
+    assert bool((slots == -1).all()) and bool((pos == -1).all())
+
+
 # -------------------------------------------------------------------------------------------
 # paged append
 # -------------------------------------------------------------------------------------------

@@ -734,7 +734,7 @@ def _heads(x, name):
     shape, stride = x.shape, x.stride()
     if len(shape) != 3:
         raise ValueError(f"{name} must be [T, heads, d]")
-    if stride[2] != 1 or stride[1] != shape[2]:
+    if stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return shape, stride[0]
 

@@ -333,6 +333,20 @@ def test_no_lse_and_given_workspace():
         m.run(ws=ws[:need - 16])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_head_of_any_stride(dtype):
+    """[heads, T, d] seen as [T, heads, d] with one head: the stride of the heads says nothing."""
+    m = Batch(14, dtype, 1, 1, 64, 16, 100, [1, 3, 20], [5, 30, 40])
+    q = m.q.as_strided(m.q.shape, (m.d, len(m.q) * m.d, 1))
+    assert q.stride(1) != m.d
+    m.q = q
+    m.check(*m.run())
+    slots = torch.arange(len(q), device=DEV, dtype=torch.int32)
+    k, v = (torch.zeros(2, 1, 16, 64, device=DEV, dtype=dtype) for _ in range(2))
+    bsa.paged_append(q, q, slots, k, v)
+    assert torch.equal(k.view(-1, 64)[:len(q)], q[:, 0]) and torch.equal(k, v)
+
+
 # -------------------------------------------------------------------------------------------
 # page tables
 # -------------------------------------------------------------------------------------------

@@ -822,12 +822,13 @@ def _prefix_attn_bytes(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q):
 
 def prefix_attn_workspace_bytes(dtype, T, B, Hq, Hk, d, page, table_ld, prefix_len,
                                 max_q=1) -> int:
-    """Workspace bytes of prefix_attn for these sizes."""
+    """Workspace bytes of prefix_attn for these sizes (max_q: T for a call with cu_q and no
+    max_q)."""
     dt = BSA_BF16 if dtype == torch.bfloat16 else BSA_F32
     return _prefix_attn_bytes(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q)
 
 
-def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q=None, max_q=1,
+def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q=None, max_q=None,
                 o=None, lse=None, ws=None, status=None):
     """Attention of a batch behind a shared prefix, over pages (bsa_prefix_attn).
 
@@ -835,9 +836,12 @@ def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q
     [num_pages, Hk, page, d]; table [B, ld], lens [B]: each request's own pages and tokens, the new
     ones included; prefix_table, prefix_len: the shared prefix (prefix_table may be None when
     prefix_len is 0).  cu_q [B + 1]: first new token of each request, with max_q the most any
-    request has; None: one token per request.  ``ws``: a uint8 device tensor of at least
-    prefix_attn_workspace_bytes bytes (allocated here when None).  ``status`` (int32 [1], optional):
-    set nonzero if a bounded device wait ran out.  Returns (o, lse)."""
+    request has (None: T, which always holds; the plan is better with the number itself); without
+    cu_q: one token per request.  Rows that cu_q gives to no request (padding behind the last,
+    tokens before the first or beyond max_q) are left as they were: undefined in an o and lse
+    allocated here.  ``ws``: a uint8 device tensor of at least prefix_attn_workspace_bytes bytes
+    (allocated here when None).  ``status`` (int32 [1], optional): set nonzero if a bounded device
+    wait ran out.  Returns (o, lse)."""
     shape, q_stride = _heads(q, "q")
     T, Hq, d = shape
     pool = k_pages.shape
@@ -850,6 +854,8 @@ def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q
         raise ValueError("table must be [B, ld]")
     if cu_q is not None and cu_q.numel() != B + 1:
         raise ValueError("cu_q must be [B + 1]")
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(T, 1)
     if prefix_len > 0 and (prefix_table is None or prefix_table.numel() * page < prefix_len):
         raise ValueError("prefix_table must list ceil(prefix_len / page) pages")
     dtype = q.dtype

@@ -106,6 +106,17 @@ def test_each_kernel(dtype, d, heads, kv_heads, page, prefix, B, most, own, laun
     m.check(*m.run())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("prefix", [0, 700])
+@pytest.mark.parametrize("nq", [[1, 5, 0, 8, 3], [40, 1, 129, 64, 2], [1, 1, 0, 1, 1]])
+def test_most_new_tokens_need_not_be_named(dtype, prefix, nq):
+    """cu_q without max_q: every token of every request is attended."""
+    m = Batch(33, dtype, 8, 2, 64, 16, prefix, nq, [max(n, 30) + i for i, n in enumerate(nq)])
+    o = torch.full_like(m.q, float("nan"))
+    _, lse = bsa.prefix_attn(m.q, m.k, m.v, m.table, m.lens, m.prefix_table, prefix, cu_q=m.cu, o=o)
+    m.check(o, lse)
+
+
 FAR = [
     (BF16, 130, 3, 1, 40, ["rows128x1"]), (BF16, 130, 70, 1, 200, ["rows128x1", "merge"]),
     (BF16, 20001, 40, 1, 100, ["tc128", "rows128x1", "merge"]),

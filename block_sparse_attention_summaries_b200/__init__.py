@@ -74,6 +74,8 @@ SIGNATURES = [
                               _I, _P, _P, _P]),
     ("bsa_prefix_attn", _I, [_P, ctypes.c_longlong, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I,
                              _P, _P, _I, _P, _I, _P, _P, _P, _P, _Z, _P]),
+    ("bsa_prefix_attn_slots", _I, [_P, ctypes.c_longlong, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                                   _P, _I, _P, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _Z, _P]),
     ("bsa_prefix_attn_workspace_bytes", _Z, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I]),
     ("bsa_workspace_status", _I, [_P, _P]),
     ("bsa_selftest_bounded_wait", _I, [_P, _I, _P]),
@@ -757,7 +759,9 @@ def page_tables(lens, new_lens, table, ring, free, page, max_tokens, pos_offset=
 
     lens, new_lens [B], table [B, ld], ring [num_pages], free [2] = (head, avail): int32.  Every
     request goes from lens to new_lens tokens; ``table`` and ``ring`` are updated in place.
-    ``status`` (int32 [1], optional) collects PAGES_* bits.  Returns (lens_out [B], free_out [2],
+    ``status`` (int32 [1], optional) collects PAGES_* bits.  Tokens of a request that finds no pages,
+    and those past max_tokens, have slot -1: pass the slots on to paged_append and prefix_attn.
+    Returns (lens_out [B], free_out [2],
     cu_new [B + 1], slots [max_tokens], positions [max_tokens]); pass lens_out=lens and
     free_out=free to advance the state in place."""
     dev = _device_index(lens)
@@ -829,7 +833,7 @@ def prefix_attn_workspace_bytes(dtype, T, B, Hq, Hk, d, page, table_ld, prefix_l
 
 
 def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q=None, max_q=None,
-                o=None, lse=None, ws=None, status=None):
+                o=None, lse=None, ws=None, status=None, slots=None):
     """Attention of a batch behind a shared prefix, over pages (bsa_prefix_attn).
 
     q [T, Hq, d]: the new tokens, packed (tokens may be strided); k_pages, v_pages
@@ -839,7 +843,9 @@ def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q
     request has (None: T, which always holds; the plan is better with the number itself); without
     cu_q: one token per request.  Rows that cu_q gives to no request (padding behind the last,
     tokens before the first or beyond max_q) are left as they were: undefined in an o and lse
-    allocated here.  ``ws``: a uint8 device tensor of at least prefix_attn_workspace_bytes bytes
+    allocated here.  ``slots`` (int32, optional): the step's slots as page_tables returned them; a
+    token without one (its request was refused, or max_tokens was too small) gets o = 0, lse = -inf
+    instead of passing for its request's last token.  ``ws``: a uint8 device tensor of at least prefix_attn_workspace_bytes bytes
     (allocated here when None).  ``status`` (int32 [1], optional): set nonzero if a bounded device
     wait ran out.  Returns (o, lse)."""
     shape, q_stride = _heads(q, "q")
@@ -883,12 +889,15 @@ def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q
         raise ValueError("ws must be uint8")
     else:
         _on_device(dev, ws)
-    _on_device(dev, k_pages, v_pages, table, lens, prefix_table, cu_q, status)
-    _ints(table, lens, prefix_table, cu_q, status)
-    _call(lib().bsa_prefix_attn, dev, "bsa_prefix_attn", q.data_ptr(), q_stride,
+    _on_device(dev, k_pages, v_pages, table, lens, prefix_table, cu_q, status, slots)
+    _ints(table, lens, prefix_table, cu_q, status, slots)
+    num_slots = 0 if slots is None else slots.numel()
+    # an empty tensor has no address, but it is one: no token has a slot
+    at = None if slots is None else slots.data_ptr() or lens.data_ptr()
+    _call(lib().bsa_prefix_attn_slots, dev, "bsa_prefix_attn", q.data_ptr(), q_stride,
           k_pages.data_ptr(), v_pages.data_ptr(), dt, T, B, Hq, Hk, d, page, P, table.data_ptr(),
           table_ld, lens.data_ptr(), None if prefix_table is None else prefix_table.data_ptr(),
-          prefix_len, None if cu_q is None else cu_q.data_ptr(), max_q, o.data_ptr(),
+          prefix_len, None if cu_q is None else cu_q.data_ptr(), max_q, at, num_slots, o.data_ptr(),
           lse.data_ptr(), None if status is None else status.data_ptr(), ws.data_ptr(),
           ws.numel())
     return o, lse

@@ -528,15 +528,15 @@ extern "C" size_t bsa_prefix_attn_workspace_bytes(bsa_dtype dt, int T, int B, in
   return w.bytes();
 }
 
-extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const void* k_pages,
-                                      const void* v_pages, bsa_dtype dt, int T, int B, int Hq,
-                                      int Hk, int d, int page, int num_pages, const int* table,
-                                      int table_ld, const int* lens, const int* prefix_table,
-                                      int prefix_len, const int* cu_q, int max_q, void* o,
-                                      float* lse, int* status, void* workspace,
-                                      size_t workspace_bytes, void* stream) {
+extern "C" bsa_status bsa_prefix_attn_slots(
+    const void* q, long long q_stride, const void* k_pages, const void* v_pages, bsa_dtype dt, int T,
+    int B, int Hq, int Hk, int d, int page, int num_pages, const int* table, int table_ld,
+    const int* lens, const int* prefix_table, int prefix_len, const int* cu_q, int max_q,
+    const int* slots, int num_slots, void* o, float* lse, int* status, void* workspace,
+    size_t workspace_bytes, void* stream) {
   BSA_REQUIRE(sizes_ok(T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q) && num_pages >= 1,
               BSA_ERR_ARG);
+  BSA_REQUIRE(num_slots >= 0, BSA_ERR_ARG);
   BSA_REQUIRE(dtype_ok(dt), BSA_ERR_DTYPE);
   BSA_REQUIRE(T == 0 || B == 0 || (q && k_pages && v_pages && lens && o), BSA_ERR_ARG);
   BSA_REQUIRE(prefix_len == 0 || prefix_table, BSA_ERR_ARG);
@@ -568,6 +568,7 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
   p.table = table; p.table_ld = table_ld; p.lens = lens;
   p.ptable = prefix_table; p.prefix_len = prefix_len;
   p.cu_q = cu_q; p.max_q = max_q;
+  p.slots = slots; p.num_slots = num_slots;
   p.o = o; p.lse = lse;
   BSA_REQUIRE(w.items <= INT_MAX - kRowsCtas, BSA_ERR_UNSUPPORTED);
   char* ws = static_cast<char*>(workspace);
@@ -588,4 +589,16 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
                    : launch_parts<__nv_bfloat16, 128>(p, w, status, st);
   return d == 64 ? launch_parts<float, 64>(p, w, status, st)
                  : launch_parts<float, 128>(p, w, status, st);
+}
+
+extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const void* k_pages,
+                                      const void* v_pages, bsa_dtype dt, int T, int B, int Hq,
+                                      int Hk, int d, int page, int num_pages, const int* table,
+                                      int table_ld, const int* lens, const int* prefix_table,
+                                      int prefix_len, const int* cu_q, int max_q, void* o,
+                                      float* lse, int* status, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  return bsa_prefix_attn_slots(q, q_stride, k_pages, v_pages, dt, T, B, Hq, Hk, d, page, num_pages,
+                               table, table_ld, lens, prefix_table, prefix_len, cu_q, max_q, nullptr,
+                               0, o, lse, status, workspace, workspace_bytes, stream);
 }

@@ -21,6 +21,8 @@ struct PrefixParams {
   int prefix_len;
   const int* cu_q;  // [B + 1] or null: one new token per request
   int max_q;
+  const int* slots;  // [num_slots] or null: the places of the new tokens (pa_placed)
+  int num_slots;
   void* o;
   float* lse;
   // Partial results: slots [0, ns1) hold the pieces of the prefix, [ns1, ns1 + ns2) those of the
@@ -110,6 +112,16 @@ __device__ __forceinline__ int pa_tokens(const PrefixParams& p) {
   return p.cu_q ? min(max(p.cu_q[p.B], 0), p.T) : p.B;
 }
 
+// Whether token t has a place in the cache.  One without (its request was refused pages, or no slot
+// was left for it) has no position either: where it would stand by its request's length, another
+// token is.
+__device__ __forceinline__ bool pa_placed(const int* slots, int num_slots, int places, int t) {
+  return !slots || (t < num_slots && (unsigned)slots[t] < (unsigned)places);
+}
+__device__ __forceinline__ bool pa_placed(const PrefixParams& p, int t) {
+  return pa_placed(p.slots, p.num_slots, p.num_pages << p.page_shift, t);
+}
+
 // Joins the pieces of row (token t, query head hq) and writes o and lse: a warp, d / 32 columns per
 // lane.  t is a token of a request.
 template <typename T, int D>
@@ -146,7 +158,7 @@ __device__ __forceinline__ void pa_join_row(const PrefixParams& p, int t, int hq
     const PaRequest r = pa_request(p, b);
     if (pa_own_keys(p, r) > 0) pieces(false, b, ((t - r.t0) << p.g_shift) + g, first1, count1);
   }
-  const int ns = p.ns1 + p.ns2, n = ns + count0 + count1;
+  const int ns = p.ns1 + p.ns2, n = pa_placed(p, t) ? ns + count0 + count1 : 0;
   auto piece = [&](int s, const float2*& ml, const float*& o) {
     if (s < ns) {
       const long long i = s * rows + row;

@@ -212,14 +212,16 @@ __device__ __forceinline__ Unit unit_of(const PrefixParams& p, const TcGrid& g) 
 
 // Adds the infinities and NaNs of V at own keys [j0, n) to the results (o, or else part) of the
 // rows that see them: a warp.  Not inline and by value, so that it takes no register of the other
-// roles.
+// roles.  o is final: rows of tokens without a place keep their 0.
 template <int D>
 __device__ __noinline__ void add_cleaned(const __nv_bfloat16* v, const int* pages, int num_pages,
                                          int page_shift, int Hk, int h, int j0, int n,
                                          int first_pos, int r0, int nrows, int g_shift, int Hq,
-                                         __nv_bfloat16* o, float* part) {
+                                         __nv_bfloat16* o, float* part, const int* slots,
+                                         int num_slots) {
   for (int i = threadIdx.x & 31; i < nrows * D; i += 32) {
     const int row = i / D, c = i % D, rr = r0 + row;
+    if (o && !pa_placed(slots, num_slots, num_pages << page_shift, rr >> g_shift)) continue;
     const int end = min(n, first_pos + (row >> g_shift) + 1);
     float add = 0.f;
     for (int j = j0; j < end; ++j) {
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       add_cleaned<D>(static_cast<const __nv_bfloat16*>(p.v), u.own, p.num_pages, p.page_shift, p.Hk,
                      u.h, j0, min(u.n1, (u.tile1 - u.tiles0) * kXKeys), u.first_pos, u.r0, u.nrows,
                      p.g_shift, p.Hq, g.direct ? static_cast<__nv_bfloat16*>(p.o) : nullptr,
-                     p.part_o + (size_t)u.slot * rows * D);
+                     p.part_o + (size_t)u.slot * rows * D, p.slots, p.num_slots);
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kXRegsSoftmax));
@@ -622,6 +624,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       stage = smem + L::kRing + warp * (L::kTile / 4);  // both streams have read the ring
     }
     const bool live = row < u.nrows;
+    if (g.direct && live && !pa_placed(p, (u.r0 + row) >> p.g_shift)) l = 0.f;  // as without keys
     if (live && (wide || s == 0)) {
       const long long id = row_id(row);
       if (!g.direct) p.part_ml[u.slot * rows + id] = make_float2(m, l);

@@ -505,7 +505,7 @@ size_t bsa_freesolo_workspace_bytes(bsa_dtype dt, int B, int H, int n, int d, in
  * lists, in order, and all requests of a batch read the pages of a common prefix (a system prompt,
  * a document), which are stored once.  They serve the layers that keep full attention beside the
  * block-sparse ones.  The pages cited above have no counterpart to them.  A serving step is
- *     bsa_page_tables -> bsa_paged_append -> bsa_prefix_attn
+ *     bsa_page_tables -> bsa_paged_append -> bsa_prefix_attn (or ..._slots)
  * on one stream; nothing in it reads device memory on the host, so it can be captured into a graph.
  */
 
@@ -538,6 +538,12 @@ typedef enum {
  *             length of the shared prefix), -1 where there is none.
  *   status    optional device int: bsa_pages_status bits are or-ed into it.
  * lens_out may be lens or new_lens, and free_out may be free_in (a state advanced in place).
+ * A request that is not served keeps its tokens' places in cu_new, and tokens past max_tokens have
+ * none: both are tokens of the step without a slot.  bsa_paged_append skips them, and
+ * bsa_prefix_attn_slots answers them with o = 0 and lse = -inf.  (bsa_prefix_attn, which is not told,
+ * would take those of a refused request for its last tokens.)  Past max_tokens lens_out counts the
+ * tokens all the same, and their pages are theirs: a caller that sees BSA_PAGES_TOKENS writes
+ * their keys and values, or goes back to the lengths before, before a later step attends to them.
  * Limits: B <= 8192, num_pages * page < 2^31.  Deterministic; one launch.
  */
 bsa_status bsa_page_tables(int B, int page, const int* lens, const int* new_lens, int* table,
@@ -592,7 +598,22 @@ bsa_status bsa_prefix_attn(const void* q, long long q_stride, const void* k_page
                            const int* cu_q, int max_q, void* o, float* lse, int* status,
                            void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes bsa_prefix_attn needs for these sizes (0 for unsupported ones). */
+/*
+ * bsa_prefix_attn_slots -- bsa_prefix_attn for a step some of whose tokens may have no place in the
+ * cache (bsa_page_tables found no pages for their request, or no slot for them).
+ *   slots     [num_slots] optional: the slots of the T new tokens, as bsa_page_tables wrote them.  A
+ *             token whose slot is outside [0, num_pages * page), or that lies at or past num_slots,
+ *             gets o = 0, lse = -inf; the others are attended as by bsa_prefix_attn.
+ */
+bsa_status bsa_prefix_attn_slots(const void* q, long long q_stride, const void* k_pages,
+                                 const void* v_pages, bsa_dtype dt, int T, int B, int Hq, int Hk,
+                                 int d, int page, int num_pages, const int* table, int table_ld,
+                                 const int* lens, const int* prefix_table, int prefix_len,
+                                 const int* cu_q, int max_q, const int* slots, int num_slots,
+                                 void* o, float* lse, int* status, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/* Workspace bytes bsa_prefix_attn (or ..._slots) needs for these sizes (0 for unsupported ones). */
 size_t bsa_prefix_attn_workspace_bytes(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page,
                                        int table_ld, int prefix_len, int max_q);
 

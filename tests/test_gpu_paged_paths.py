@@ -117,6 +117,110 @@ def test_most_new_tokens_need_not_be_named(dtype, prefix, nq):
     m.check(o, lse)
 
 
+# as PATHS: each way in which a row's result is written
+PLACES = [
+    (BF16, 64, 8, 2, 32, 100, 5, 1, 40, ["rows64x1"]),
+    (BF16, 128, 8, 2, 128, 8191, 24, 8, 700, ["tc128", "rows128x2", "merge"]),
+    (BF16, 128, 8, 2, 128, 701, 3, 300, 400, ["tc128", "merge"]),
+    (BF16, 64, 16, 4, 64, 700, 12, 260, 300, ["tc64"]),
+    (BF16, 128, 16, 4, 32, 699, 12, 260, 300, ["tc128"]),
+    (F32, 64, 8, 2, 16, 50, 2, 1, 40, ["simt64:16:16"]),
+    (F32, 64, 8, 2, 32, 701, 6, 70, 300, ["simt64:64:64", "merge"]),
+]
+
+
+@pytest.mark.parametrize("dtype,d,heads,kv_heads,page,prefix,B,most,own,launched", PLACES)
+@pytest.mark.parametrize("cut", [0, 1, None])
+def test_tokens_without_a_slot(dtype, d, heads, kv_heads, page, prefix, B, most, own, launched, cut):
+    """A refused request's tokens, single tokens on pages outside the pool and those past the end
+    of `slots` are answered with nothing; the others as without `slots`, to the bit."""
+    nq, lens = ragged(B + most, B, most, own)
+    m = Batch(34, dtype, heads, kv_heads, d, page, prefix, nq, lens, decode=most == 1, pad_tokens=0)
+    m.v[int(m.own_ids[1][0]), :, 0] = float("inf")  # of tokens with a slot and without
+    o, lse = m.run()
+    T = m.q.shape[0]
+    top = m.k.shape[0] * page
+    slots = np.arange(T) % top
+    slots[0] = top - 1
+    c = m.cu_list
+    slots[c[1] + nq[1] // 2:c[2]] = -1
+    slots[T - 1] = top  # behind the pool
+    if most > 1:
+        slots[1] = 2**31 - 1
+    n = {0: 0, 1: T - 1, None: T}[cut]
+    none = (slots < 0) | (slots >= top) | (np.arange(T) >= n)
+    given = torch.tensor(slots[:n].astype(np.int32), device=DEV)
+    got, got_lse = m.run(slots=given)
+    assert kernels(lambda: m.run(slots=given)) == launched
+    none = torch.as_tensor(none, device=DEV)
+    assert none.any() and (n == 0 or not none.all())
+    assert (got[none] == 0).all() and (got_lse[none] == -float("inf")).all()
+    assert torch.equal(got[~none].view(torch.uint8), o[~none].view(torch.uint8))
+    assert torch.equal(got_lse[~none], lse[~none])
+
+
+class PlacedServer(Server):
+    """Hands the slots on, and checks a step whose pages or places may run out."""
+
+    def step(self, q, k, v, new_lens, max_tokens, max_q):
+        _, _, cu, slots, _ = bsa.page_tables(self.lens, new_lens, self.table, self.ring, self.free,
+                                             self.page, max_tokens, lens_out=self.lens,
+                                             free_out=self.free, status=self.status)
+        bsa.paged_append(k[:max_tokens], v[:max_tokens], slots, self.k, self.v)
+        return bsa.prefix_attn(q, self.k, self.v, self.table, self.lens, self.prefix_table,
+                               self.prefix, cu_q=cu, max_q=max_q, slots=slots)
+
+    def moves(self, adds, refused=(), places=None):
+        """adds: new tokens of each request (None: done); returns the status bits of the step."""
+        before = self.lens.cpu().numpy()
+        new = [0 if a is None else int(n) + a for n, a in zip(before, adds)]
+        nq = [a or 0 for a in adds]
+        T = sum(nq)
+        q, k, v = (self.randn(T, h, self.d) for h in (self.heads, self.kv_heads, self.kv_heads))
+        self.status.zero_()
+        places = T if places is None else places
+        o, lse = self.step(q, k, v, torch.tensor(new, dtype=torch.int32, device=DEV), places,
+                           max(nq))
+        at = 0
+        for b, n in enumerate(nq):
+            if adds[b] is None:
+                self.own[b] = (self.randn(0, self.kv_heads, self.d),) * 2
+            put = 0 if b in refused else max(0, min(n, places - at))  # tokens in the cache
+            assert (o[at + put:at + n] == 0).all()
+            assert (lse[at + put:at + n] == -float("inf")).all()
+            if put:
+                self.record(b, k[at:at + put], v[at:at + put])
+                want, tol = self.want(b, q[at:at + put])
+                assert ((o[at:at + put].double() - want).abs() <= tol).all(), b
+            at += n
+        return int(self.status)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("prefix", [100, 40001])
+def test_steps_with_refused_requests(dtype, prefix):
+    """Tables, append and attention when pages run out: the refused requests' tokens are answered
+    with nothing, the others are served, and the refused ones too once there are pages."""
+    s = PlacedServer(dtype=dtype, B=3, prefix=prefix, pool=-(-prefix // 16) + 6)
+    assert s.moves([30, 20, 33], refused=[2]) == bsa.PAGES_EXHAUSTED  # 2 + 2 + 3 of 6 pages
+    assert s.moves([1, None, 32]) == 0  # takes the last two, frees two
+    assert s.lens.tolist() == [31, 0, 32]
+    # as many old tokens as new ones, so that every position exists
+    assert s.moves([18, 0, 28], refused=[2]) == bsa.PAGES_EXHAUSTED
+    assert s.lens.tolist() == [49, 0, 32]
+    assert s.moves([None, 0, 1], refused=[2]) == bsa.PAGES_EXHAUSTED
+    assert s.moves([0, 9, 28]) == 0
+    assert s.lens.tolist() == [0, 9, 60]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_step_with_too_few_places(dtype):
+    """More new tokens than max_tokens: the ones without a slot are answered with nothing."""
+    s = PlacedServer(dtype=dtype, B=3)
+    assert s.moves([20, 30, 11], places=45) == bsa.PAGES_TOKENS
+    assert s.lens.tolist() == [20, 30, 11]
+
+
 FAR = [
     (BF16, 130, 3, 1, 40, ["rows128x1"]), (BF16, 130, 70, 1, 200, ["rows128x1", "merge"]),
     (BF16, 20001, 40, 1, 100, ["tc128", "rows128x1", "merge"]),

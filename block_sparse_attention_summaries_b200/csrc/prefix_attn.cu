@@ -503,6 +503,8 @@ bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status,
              : BSA_ERR_CUDA;
 }
 
+thread_local uint32_t t_polls = kPaPolls;  // set by the self-test alone
+
 constexpr int kMaxKeys = INT_MAX - 1024;  // room to round up to tiles
 
 bool sizes_ok(int T, int B, int Hq, int Hk, int d, int page, int table_ld, int prefix_len,
@@ -569,6 +571,7 @@ extern "C" bsa_status bsa_prefix_attn_slots(
   p.ptable = prefix_table; p.prefix_len = prefix_len;
   p.cu_q = cu_q; p.max_q = max_q;
   p.slots = slots; p.num_slots = num_slots;
+  p.polls = t_polls;
   p.o = o; p.lse = lse;
   BSA_REQUIRE(w.items <= INT_MAX - kRowsCtas, BSA_ERR_UNSUPPORTED);
   char* ws = static_cast<char*>(workspace);
@@ -601,4 +604,9 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
   return bsa_prefix_attn_slots(q, q_stride, k_pages, v_pages, dt, T, B, Hq, Hk, d, page, num_pages,
                                table, table_ld, lens, prefix_table, prefix_len, cu_q, max_q, nullptr,
                                0, o, lse, status, workspace, workspace_bytes, stream);
+}
+
+extern "C" bsa_status bsa_selftest_prefix_waits(int polls) {
+  t_polls = polls < 0 ? kPaPolls : (uint32_t)polls;
+  return BSA_OK;
 }

@@ -285,10 +285,10 @@ __global__ void __launch_bounds__(kRThreads, 2)
       const int y = ((id * p.Hk + kh) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
       for (int kv = 0; kv < 2 && ok; ++kv) {
         const int sl = k % L::kSlots;
-        if (k >= L::kSlots) ok = mbar_wait_bounded(&empty[sl], ((k / L::kSlots) - 1) & 1);
+        if (k >= L::kSlots) ok = pa_wait(p, &empty[sl], ((k / L::kSlots) - 1) & 1);
         const bool queries = first && kv == 0;
         if (queries && piece >= L::kQBufs)
-          ok = ok && mbar_wait_bounded(&q_free[qb], ((piece / L::kQBufs) - 1) & 1);
+          ok = ok && pa_wait(p, &q_free[qb], ((piece / L::kQBufs) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
@@ -344,8 +344,8 @@ __global__ void __launch_bounds__(kRThreads, 2)
     for (int i = 0; i < count; ++i, k += 2) {
       const int buf = i & 1;
       const int ks = k % L::kSlots, vs = (k + 1) % L::kSlots;
-      bool ok = mbar_wait_bounded(&full[ks], (k / L::kSlots) & 1) &&
-                mbar_wait_bounded(&full[vs], ((k + 1) / L::kSlots) & 1);
+      bool ok = pa_wait(p, &full[ks], (k / L::kSlots) & 1) &&
+                pa_wait(p, &full[vs], ((k + 1) / L::kSlots) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         // the consumers stop together, behind the tile's first barrier

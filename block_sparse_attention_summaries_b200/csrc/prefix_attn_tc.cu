@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = smem_align1024(smem_raw);
-  __shared__ __align__(8) uint64_t bars[2 * L::kSlots + kXMasks + 9 + kXMend];
+  __shared__ __align__(8) uint64_t bars[2 * L::kSlots + kXMasks + 10 + kXMend];
   uint64_t* full = bars;
   uint64_t* empty = full + L::kSlots;
   uint64_t* mask_full = empty + L::kSlots;  // page mask of a key tile written
@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
   uint64_t* s_full = q_full + 1;  // [2]
   uint64_t* p_full = s_full + 2;  // [stream][part]
   uint64_t* o_done = p_full + 4;  // [2]
-  uint64_t* mended = o_done + 2;  // V of a tile is fit for its product
+  uint64_t* fin = o_done + 2;     // every product issued is complete
+  uint64_t* mended = fin + 1;     // V of a tile is fit for its product
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ int s_dirty;  // first own key of a tile of V that was cleaned
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     for (int i = 0; i < kXMasks; ++i) mbar_init(&mask_full[i], 1);
     for (int i = 0; i < kXMend; ++i) mbar_init(&mended[i], 1);
     mbar_init(q_full, 1);
+    mbar_init(fin, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[2 * s], 4);
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       }
       for (int kv = 0; kv < 2; ++kv, ++k) {
         const int sl = k % L::kSlots;
-        if (k >= L::kSlots) ok = mbar_wait_bounded(&empty[sl], ((k / L::kSlots) - 1) & 1);
+        if (k >= L::kSlots) ok = pa_wait(p, &empty[sl], ((k / L::kSlots) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0)
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       if (!ok || !mends(i)) continue;
       // the tile's V, once it is there
       const int kv = k - 1, sl = kv % L::kSlots;
-      ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[sl], (kv / L::kSlots) & 1));
+      ok = __all_sync(0xffffffffu, pa_wait(p, &full[sl], (kv / L::kSlots) & 1));
       if (!ok) break;
       unsigned char* vt = slot_at(sl);
       const int j0 = j0_at(i), left = left_at(i);
@@ -416,6 +418,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     }
     if (!ok && lane == 0) s_abort = 1;
     // copies still in flight land before the CTA leaves, whatever the other roles do
+    (void)mbar_wait_bounded(q_full, 0);
     for (int j = max(0, k - L::kSlots); j < k; ++j)
       (void)mbar_wait_bounded(&full[j % L::kSlots], (j / L::kSlots) & 1);
   } else if (warp == 9) {
@@ -427,8 +430,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const uint32_t q_lo = desc_lo(smem_u32(smem + L::kQ), 16);
     const uint32_t q_next = wide ? L::kTile >> 4 : 0;  // to the second stream's queries
     auto ready = [&](int k) {
-      return __all_sync(0xffffffffu,
-                        mbar_wait_bounded(&full[k % L::kSlots], (k / L::kSlots) & 1));
+      return __all_sync(0xffffffffu, pa_wait(p, &full[k % L::kSlots], (k / L::kSlots) & 1));
     };
     // S_s of the stream's step i
     auto issue_s = [&](int s, int i) -> bool {
@@ -447,10 +449,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
       if (!wide || s == 1) commit_one(leader, empty0 + 8 * sl);
       return true;
     };
-    bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_full, 0));
+    bool ok = __all_sync(0xffffffffu, pa_wait(p, q_full, 0));
     int nmend = 0;
+    bool any = false;  // products issued
     for (int s = 0; s < 2 && ok; ++s)
-      if (steps(s) > 0) ok = issue_s(s, 0);
+      if (steps(s) > 0) any |= (ok = issue_s(s, 0));
     for (int i = 0; i < steps(0) && ok; ++i) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -460,15 +463,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (!ok) continue;
         // a tile of V that the producer mends first, once per tile
         if ((!wide || s == 0) && mends(ti)) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&mended[nmend % kXMend],
-                                                         (nmend / kXMend) & 1));
+          ok = __all_sync(0xffffffffu, pa_wait(p, &mended[nmend % kXMend], (nmend / kXMend) & 1));
           ++nmend;
           if (!ok) continue;
         }
         const uint32_t b = desc_lo(ring + sl * L::kTile, 16384);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
-          ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&p_full[2 * s + part], i & 1));
+          ok = ok && __all_sync(0xffffffffu, pa_wait(p, &p_full[2 * s + part], i & 1));
           if (!ok) break;
           tc::fence_after_sync();
 #pragma unroll
@@ -484,8 +486,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
     // Every product issued is complete, and every arrival that waits for one is made, before TMEM
     // and shared memory are given up: an arrival behind the CTA's end would hit the next CTA's
     // barriers.
-    commit_one(leader, smem_u32(q_full));
-    ok = __all_sync(0xffffffffu, mbar_wait_bounded(q_full, 1)) && ok;
+    if (any) {
+      commit_one(leader, smem_u32(fin));
+      ok = __all_sync(0xffffffffu, mbar_wait_bounded(fin, 0)) && ok;
+    }
     if (!ok && lane == 0) s_abort = 1;
   } else if (warp == 10) {
     // ------------------------------------- adds what was cleaned to the rows that do see it
@@ -510,8 +514,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     bool ok = true;
     for (int i = 0; i < ns; ++i) {
       const int ti = tile_at(s, i), t = u.tile0 + ti;
-      ok = mbar_wait_bounded(&mask_full[ti % kXMasks], (ti / kXMasks) & 1) &&
-           mbar_wait_bounded(&s_full[s], i & 1);
+      ok = pa_wait(p, &mask_full[ti % kXMasks], (ti / kXMasks) & 1) && pa_wait(p, &s_full[s], i & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();
@@ -597,7 +600,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[2 * s + 1]);
     }
-    if (ok && ns > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&o_done[s], 0));
+    if (ok && ns > 0) ok = __all_sync(0xffffffffu, pa_wait(p, &o_done[s], 0));
     if (!ok) {
       s_abort = 1;
       m = 0.f;

@@ -221,6 +221,50 @@ def test_step_with_too_few_places(dtype):
     assert s.lens.tolist() == [20, 30, 11]
 
 
+# as PATHS: each way in which a CTA of the tensor-core kernels can give up
+WAITS = [
+    (BF16, 64, 8, 2, 32, 100, 5, 1, 40, ["rows64x1"]),
+    (BF16, 64, 8, 1, 16, 100, 5, 8, 40, ["rows64x4"]),
+    (BF16, 128, 8, 2, 128, 333, 70, 8, 120, ["rows128x2", "merge"]),
+    (BF16, 128, 8, 2, 64, 33001, 20, 1, 500, ["tc128", "rows128x1", "merge"]),
+    (BF16, 64, 8, 2, 16, 20001, 40, 8, 301, ["tc64", "rows64x2", "merge"]),
+    (BF16, 128, 8, 2, 128, 701, 3, 300, 400, ["tc128", "merge"]),
+    (BF16, 128, 8, 8, 16, 1500, 20, 70, 300, ["tc128", "merge"]),
+    (BF16, 64, 16, 4, 64, 700, 12, 260, 300, ["tc64"]),
+    (BF16, 128, 16, 4, 32, 699, 12, 260, 300, ["tc128"]),
+]
+
+
+@pytest.fixture
+def no_waiting(bsa_lib):
+    """Waits between the roles of a CTA run out at once."""
+    yield lambda: bsa_lib.bsa_selftest_prefix_waits(0)
+    bsa_lib.bsa_selftest_prefix_waits(-1)
+
+
+@pytest.mark.parametrize("dtype,d,heads,kv_heads,page,prefix,B,most,own,launched", WAITS)
+def test_waits_that_run_out(no_waiting, bsa_lib, dtype, d, heads, kv_heads, page, prefix, B, most,
+                            own, launched):
+    """The kernels end, the status says so, and the next call is as the one before."""
+    nq, lens = ragged(B + most, B, most, own)
+    m = Batch(35, dtype, heads, kv_heads, d, page, prefix, nq, lens, decode=most == 1)
+    assert kernels(m.run) == launched
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    need = bsa.prefix_attn_workspace_bytes(dtype, len(m.q), B, heads, kv_heads, d, page,
+                                           m.table.shape[1], prefix, m.max_q)
+    ws = torch.empty(need, device=DEV, dtype=torch.uint8)
+    o, lse = m.run(ws=ws, status=status)
+    assert int(status) == 0
+    no_waiting()
+    m.run(ws=ws, status=status)
+    bsa_lib.bsa_selftest_prefix_waits(-1)
+    assert int(status) != 0
+    status.zero_()
+    for _ in range(2):
+        again, again_lse = m.run(ws=ws, status=status)
+        assert int(status) == 0 and torch.equal(again, o) and torch.equal(again_lse, lse)
+
+
 FAR = [
     (BF16, 130, 3, 1, 40, ["rows128x1"]), (BF16, 130, 70, 1, 200, ["rows128x1", "merge"]),
     (BF16, 20001, 40, 1, 100, ["tc128", "rows128x1", "merge"]),

@@ -152,7 +152,7 @@ __device__ __forceinline__ void pa_join_row(const PrefixParams& p, int t, int hq
   if (p.item_ctas) {
     const int h = hq >> p.g_shift, g = hq & (p.G - 1);
     auto pieces = [&](bool prefix, int i, int r, long long& first, int& count) {
-      const int2 c = *pa_item_cta(p, prefix, h, i);  // cut: a run that stopped early has not set it
+      const int2 c = *pa_item_cta(p, prefix, h, i);  // cut, should lengths change under the call
       const int c0 = min(max(c.x, 0), p.item_ctas - 1), c1 = min(max(c.y, c0), p.item_ctas - 1);
       first = pa_piece_row(p, prefix, h, i, c0) + r;
       count = c1 - c0 + 1;

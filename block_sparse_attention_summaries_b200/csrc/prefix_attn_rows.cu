@@ -118,12 +118,43 @@ __device__ __noinline__ void add_cleaned(const __nv_bfloat16* v, const int* page
   }
 }
 
+// The pieces of a CTA that gave up: the tiles [f0, f1) of the call (of the cluster's head), in the
+// order in which they are dealt out.  Their rows get sum NaN, whatever was written of them, so that the
+// join cannot take what an earlier call left in the workspace for their results.  A warp; not inline:
+// it runs after a timeout only.
+__device__ __noinline__ void give_up(const PrefixParams& p, int keys, int group_rows, int heads,
+                                     int head0, int me, long long f0, long long f1) {
+  const int lane = threadIdx.x & 31;
+  long long at = 0;  // the item's first tile
+  auto item = [&](bool prefix, int h, int i, int n, int nrows) {
+    const int tiles = (n + keys - 1) / keys;
+    if (at < f1 && at + tiles > f0) {
+      if (lane == 0) {
+        if (at >= f0) pa_item_cta(p, prefix, h, i)->x = me;
+        if (at + tiles <= f1) pa_item_cta(p, prefix, h, i)->y = me;
+      }
+      const long long row = pa_piece_row(p, prefix, h, i, me);
+      for (int r = lane; r < nrows; r += 32) p.item_ml[row + r] = make_float2(0.f, NAN);
+    }
+    at += tiles;
+  };
+  for (int h = 0; h < heads; ++h)
+    for (int i = 0; i < p.groups; ++i)
+      item(true, head0 + h, i, p.prefix_len,
+           min((pa_tokens(p) << p.g_shift) - i * group_rows, group_rows));
+  for (int b = 0; b < p.B; ++b) {
+    const PaRequest r = pa_request(p, b);
+    for (int h = 0; h < heads; ++h)
+      item(false, head0 + h, b, pa_own_keys(p, r), min(r.nq, p.max_q) << p.g_shift);
+  }
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(kRThreads, 2)
     prefix_rows_kernel(const __grid_constant__ CUtensorMap tmq,
                        const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, const PrefixParams p,
-                       const RowsGrid g) {
+                       const __grid_constant__ CUtensorMap tmv,
+                       const __grid_constant__ PrefixParams p, const RowsGrid g) {
   using L = RowsSmem<D, MT>;
   constexpr int kRKeys = L::kKeys;
   constexpr int NT = D / 32;                   // 8-column output tiles of a warp
@@ -569,7 +600,10 @@ __global__ void __launch_bounds__(kRThreads, 2)
     }
   }
   __syncthreads();
-  if (s_abort && tid == 0) report_timeout(g.status, 6);
+  if (s_abort) {
+    if (tid == 0) report_timeout(g.status, 6);
+    if (warp == 0) give_up(p, kRKeys, 16 * MT, heads, head0, me, f0, f0 + count);
+  }
   if (g.after_tc) pdl_wait();  // this kernel is not complete before the one before it
   if (p.cluster) {
     // the head's pieces are all written: join its rows here

@@ -29,8 +29,8 @@
 // P is written over S in TMEM and read from there as the A operand.  S_s of step i + 1 is issued
 // behind P V_s of step i, so its completion also says that O_s may be rescaled (lazily: only when a
 // row's maximum rises by more than 2^8, else the old maximum stays and P just exceeds 1).
-// Every mbarrier wait is bounded; a role whose wait runs out stops, the unit's rows get sum NaN,
-// and the CTA reaches its last barrier and frees TMEM.
+// Every mbarrier wait is bounded; a role whose wait runs out stops, the CTA reaches its last
+// barrier, its unit's rows get NaN (of a piece: sum NaN), and it frees TMEM.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -601,11 +601,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       if (lane == 0) mbar_arrive(&p_full[2 * s + 1]);
     }
     if (ok && ns > 0) ok = __all_sync(0xffffffffu, pa_wait(p, &o_done[s], 0));
-    if (!ok) {
-      s_abort = 1;
-      m = 0.f;
-      l = NAN;
-    }
+    if (!ok) s_abort = 1;
     tc::fence_after_sync();
     // O to memory through shared memory, so that a warp writes whole rows (a thread writing its own
     // row 16 bytes at a time took 4.4 us a unit).  A deep unit's streams join their halves: TMEM
@@ -690,7 +686,20 @@ __global__ void __launch_bounds__(kXThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (s_abort && tid == 0) report_timeout(g.status, 5);
+  if (s_abort) {
+    if (tid == 0) report_timeout(g.status, 5);
+    // what the softmax warps wrote came from tiles that may not have been there
+    for (int r = tid; r < u.nrows; r += kXThreads) {
+      const long long id = row_id(r);
+      if (!g.direct) {
+        p.part_ml[u.slot * rows + id] = make_float2(0.f, NAN);
+        continue;
+      }
+      if (p.lse) p.lse[id] = NAN;
+      for (int c = 0; c < D; ++c)
+        static_cast<__nv_bfloat16*>(p.o)[id * D + c] = __float2bfloat16_rn(NAN);
+    }
+  }
   if (warp == 9) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);

@@ -245,7 +245,8 @@ def no_waiting(bsa_lib):
 @pytest.mark.parametrize("dtype,d,heads,kv_heads,page,prefix,B,most,own,launched", WAITS)
 def test_waits_that_run_out(no_waiting, bsa_lib, dtype, d, heads, kv_heads, page, prefix, B, most,
                             own, launched):
-    """The kernels end, the status says so, and the next call is as the one before."""
+    """The kernels end, the status and NaN in every row say so (the workspace holds the results of
+    the call before), and the next call is as the one before."""
     nq, lens = ragged(B + most, B, most, own)
     m = Batch(35, dtype, heads, kv_heads, d, page, prefix, nq, lens, decode=most == 1)
     assert kernels(m.run) == launched
@@ -256,9 +257,9 @@ def test_waits_that_run_out(no_waiting, bsa_lib, dtype, d, heads, kv_heads, page
     o, lse = m.run(ws=ws, status=status)
     assert int(status) == 0
     no_waiting()
-    m.run(ws=ws, status=status)
+    lost, lost_lse = m.run(ws=ws, status=status)
     bsa_lib.bsa_selftest_prefix_waits(-1)
-    assert int(status) != 0
+    assert int(status) != 0 and torch.isnan(lost).all() and torch.isnan(lost_lse).all()
     status.zero_()
     for _ in range(2):
         again, again_lse = m.run(ws=ws, status=status)

@@ -79,7 +79,7 @@ SIGNATURES = [
     ("bsa_prefix_attn_workspace_bytes", _Z, [_I, _I, _I, _I, _I, _I, _I, _I, _I, _I]),
     ("bsa_workspace_status", _I, [_P, _P]),
     ("bsa_selftest_bounded_wait", _I, [_P, _I, _P]),
-    ("bsa_selftest_prefix_waits", _I, [_I]),
+    ("bsa_selftest_prefix_timeout", _I, [_I]),
 ]
 
 _lib = None

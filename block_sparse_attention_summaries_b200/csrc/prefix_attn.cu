@@ -503,7 +503,7 @@ bsa_status launch_parts(const PrefixParams& p, const PrefixPlan& w, int* status,
              : BSA_ERR_CUDA;
 }
 
-thread_local uint32_t t_polls = kPaPolls;  // set by the self-test alone
+thread_local int t_give_up = 0;  // set by the self-test alone
 
 constexpr int kMaxKeys = INT_MAX - 1024;  // room to round up to tiles
 
@@ -571,7 +571,7 @@ extern "C" bsa_status bsa_prefix_attn_slots(
   p.ptable = prefix_table; p.prefix_len = prefix_len;
   p.cu_q = cu_q; p.max_q = max_q;
   p.slots = slots; p.num_slots = num_slots;
-  p.polls = t_polls;
+  p.give_up = t_give_up;
   p.o = o; p.lse = lse;
   BSA_REQUIRE(w.items <= INT_MAX - kRowsCtas, BSA_ERR_UNSUPPORTED);
   char* ws = static_cast<char*>(workspace);
@@ -606,7 +606,7 @@ extern "C" bsa_status bsa_prefix_attn(const void* q, long long q_stride, const v
                                0, o, lse, status, workspace, workspace_bytes, stream);
 }
 
-extern "C" bsa_status bsa_selftest_prefix_waits(int polls) {
-  t_polls = polls < 0 ? kPaPolls : (uint32_t)polls;
+extern "C" bsa_status bsa_selftest_prefix_timeout(int on) {
+  t_give_up = on != 0;
   return BSA_OK;
 }

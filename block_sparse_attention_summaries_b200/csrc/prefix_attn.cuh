@@ -9,7 +9,6 @@ namespace bsa {
 
 constexpr float kPaLog2e = 1.4426950408889634f;
 constexpr float kPaLn2 = 0.6931471805599453f;
-constexpr uint32_t kPaPolls = 1u << 20;  // tries of a bounded wait
 
 struct PrefixParams {
   const void *q, *k, *v;  // q [T, Hq, d] with token stride q_stride; pools [P, Hk, page, d]
@@ -24,7 +23,7 @@ struct PrefixParams {
   int max_q;
   const int* slots;  // [num_slots] or null: the places of the new tokens (pa_placed)
   int num_slots;
-  uint32_t polls;  // of the waits between roles (those for copies in flight at the end: the usual)
+  int give_up;  // self-test: the roles of a CTA act as if their first wait had run out
   void* o;
   float* lse;
   // Partial results: slots [0, ns1) hold the pieces of the prefix, [ns1, ns1 + ns2) those of the
@@ -44,10 +43,6 @@ struct PrefixParams {
   int item_ctas;  // CTAs that share the items, 0: no items
   int cluster;    // they are one cluster per kv head, which also joins its pieces
 };
-
-__device__ __forceinline__ bool pa_wait(const PrefixParams& p, uint64_t* bar, uint32_t parity) {
-  return mbar_wait_bounded(bar, parity, p.polls);
-}
 
 // Request b: its first new token, how many it has, its own tokens.  Values that would reach
 // outside the call's arrays are cut.

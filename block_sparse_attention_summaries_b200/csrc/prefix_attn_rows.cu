@@ -120,10 +120,12 @@ __device__ __noinline__ void add_cleaned(const __nv_bfloat16* v, const int* page
 
 // The pieces of a CTA that gave up: the tiles [f0, f1) of the call (of the cluster's head), in the
 // order in which they are dealt out.  Their rows get sum NaN, whatever was written of them, so that the
-// join cannot take what an earlier call left in the workspace for their results.  A warp; not inline:
-// it runs after a timeout only.
-__device__ __noinline__ void give_up(const PrefixParams& p, int keys, int group_rows, int heads,
-                                     int head0, int me, long long f0, long long f1) {
+// join cannot take what an earlier call left in the workspace for their results.  A warp; not inline,
+// as it runs after a timeout only.
+__device__ __noinline__ void give_up(const PrefixParams& p, int keys, int group_rows, long long f0,
+                                     long long f1) {
+  const int heads = p.cluster ? 1 : p.Hk, head0 = p.cluster ? blockIdx.x / p.item_ctas : 0;
+  const int me = p.cluster ? blockIdx.x % p.item_ctas : blockIdx.x;
   const int lane = threadIdx.x & 31;
   long long at = 0;  // the item's first tile
   auto item = [&](bool prefix, int h, int i, int n, int nrows) {
@@ -167,6 +169,7 @@ __global__ void __launch_bounds__(kRThreads, 2)
   __shared__ long long s_sum[kRThreads];
   __shared__ float s_max[2][4][16 * MT], s_l[2][4][16 * MT];
   __shared__ int s_abort, s_stop;
+  __shared__ long long s_run[2];  // the CTA's tiles
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   // Behind the tensor-core kernel the inputs are already there (it has waited for them before it
@@ -216,6 +219,10 @@ __global__ void __launch_bounds__(kRThreads, 2)
   const long long ctas = min((long long)p.item_ctas, total);
   const long long f0 = me < ctas ? total * me / ctas : 0;
   const int count = me < ctas ? (int)(total * (me + 1) / ctas - f0) : 0;
+  if (tid == 0) {
+    s_run[0] = f0;
+    s_run[1] = f0 + count;
+  }
 
   if (count == 0) {
     // nothing to attend
@@ -316,10 +323,11 @@ __global__ void __launch_bounds__(kRThreads, 2)
       const int y = ((id * p.Hk + kh) << p.page_shift) + (j & ((1 << p.page_shift) - 1));
       for (int kv = 0; kv < 2 && ok; ++kv) {
         const int sl = k % L::kSlots;
-        if (k >= L::kSlots) ok = pa_wait(p, &empty[sl], ((k / L::kSlots) - 1) & 1);
+        if (k >= L::kSlots)
+          ok = !p.give_up && mbar_wait_bounded(&empty[sl], ((k / L::kSlots) - 1) & 1);
         const bool queries = first && kv == 0;
         if (queries && piece >= L::kQBufs)
-          ok = ok && pa_wait(p, &q_free[qb], ((piece / L::kQBufs) - 1) & 1);
+          ok = ok && mbar_wait_bounded(&q_free[qb], ((piece / L::kQBufs) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
@@ -372,11 +380,13 @@ __global__ void __launch_bounds__(kRThreads, 2)
     float acc[MT][NT][4], m[MT][2], l[MT][2];
     int dirty = INT_MAX;  // first key of a tile whose V was cleaned, in this piece
     int k = 0;
-    for (int i = 0; i < count; ++i, k += 2) {
+    const int todo = p.give_up ? 0 : count;
+    if (p.give_up) s_abort = 1;
+    for (int i = 0; i < todo; ++i, k += 2) {
       const int buf = i & 1;
       const int ks = k % L::kSlots, vs = (k + 1) % L::kSlots;
-      bool ok = pa_wait(p, &full[ks], (k / L::kSlots) & 1) &&
-                pa_wait(p, &full[vs], ((k + 1) / L::kSlots) & 1);
+      bool ok = mbar_wait_bounded(&full[ks], (k / L::kSlots) & 1) &&
+                mbar_wait_bounded(&full[vs], ((k + 1) / L::kSlots) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         // the consumers stop together, behind the tile's first barrier
@@ -602,7 +612,7 @@ __global__ void __launch_bounds__(kRThreads, 2)
   __syncthreads();
   if (s_abort) {
     if (tid == 0) report_timeout(g.status, 6);
-    if (warp == 0) give_up(p, kRKeys, 16 * MT, heads, head0, me, f0, f0 + count);
+    if (warp == 0) give_up(p, kRKeys, 16 * MT, s_run[0], s_run[1]);
   }
   if (g.after_tc) pdl_wait();  // this kernel is not complete before the one before it
   if (p.cluster) {

@@ -239,12 +239,33 @@ __device__ __noinline__ void add_cleaned(const __nv_bfloat16* v, const int* page
   }
 }
 
+// The end of a CTA that gave up: its unit's rows get NaN (a piece's: sum NaN), whatever the softmax
+// warps wrote of tiles that were not there.  Not inline, and the unit is worked out again: nothing is
+// kept for this in the registers of the usual way.
+template <int D>
+__device__ __noinline__ void give_up(const PrefixParams& p, const TcGrid& g) {
+  const Unit u = unit_of(p, g);
+  if (threadIdx.x == 0) report_timeout(g.status, 5);
+  for (int r = threadIdx.x; r < u.nrows; r += kXThreads) {
+    const int rr = u.r0 + r;
+    const long long id =
+        (long long)(rr >> p.g_shift) * p.Hq + u.h * p.G + (rr & (p.G - 1));
+    if (!g.direct) {
+      p.part_ml[(long long)u.slot * p.T * p.Hq + id] = make_float2(0.f, NAN);
+      continue;
+    }
+    if (p.lse) p.lse[id] = NAN;
+    for (int c = 0; c < D; ++c)
+      static_cast<__nv_bfloat16*>(p.o)[id * D + c] = __float2bfloat16_rn(NAN);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kXThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmq,
                      const __grid_constant__ CUtensorMap tmk,
-                     const __grid_constant__ CUtensorMap tmv, const PrefixParams p,
-                     const TcGrid g) {
+                     const __grid_constant__ CUtensorMap tmv,
+                     const __grid_constant__ PrefixParams p, const __grid_constant__ TcGrid g) {
   using L = TcSmem<D>;
   constexpr int kHalves = D / 64;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -381,7 +402,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
       }
       for (int kv = 0; kv < 2; ++kv, ++k) {
         const int sl = k % L::kSlots;
-        if (k >= L::kSlots) ok = pa_wait(p, &empty[sl], ((k / L::kSlots) - 1) & 1);
+        if (k >= L::kSlots)
+          ok = !p.give_up && mbar_wait_bounded(&empty[sl], ((k / L::kSlots) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0)
@@ -395,7 +417,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
       if (!ok || !mends(i)) continue;
       // the tile's V, once it is there
       const int kv = k - 1, sl = kv % L::kSlots;
-      ok = __all_sync(0xffffffffu, pa_wait(p, &full[sl], (kv / L::kSlots) & 1));
+      ok = !p.give_up;
+      ok = __all_sync(0xffffffffu, ok && mbar_wait_bounded(&full[sl], (kv / L::kSlots) & 1));
       if (!ok) break;
       unsigned char* vt = slot_at(sl);
       const int j0 = j0_at(i), left = left_at(i);
@@ -430,7 +453,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const uint32_t q_lo = desc_lo(smem_u32(smem + L::kQ), 16);
     const uint32_t q_next = wide ? L::kTile >> 4 : 0;  // to the second stream's queries
     auto ready = [&](int k) {
-      return __all_sync(0xffffffffu, pa_wait(p, &full[k % L::kSlots], (k / L::kSlots) & 1));
+      return __all_sync(0xffffffffu, mbar_wait_bounded(&full[k % L::kSlots], (k / L::kSlots) & 1));
     };
     // S_s of the stream's step i
     auto issue_s = [&](int s, int i) -> bool {
@@ -449,7 +472,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       if (!wide || s == 1) commit_one(leader, empty0 + 8 * sl);
       return true;
     };
-    bool ok = __all_sync(0xffffffffu, pa_wait(p, q_full, 0));
+    bool ok = __all_sync(0xffffffffu, !p.give_up && mbar_wait_bounded(q_full, 0));
     int nmend = 0;
     bool any = false;  // products issued
     for (int s = 0; s < 2 && ok; ++s)
@@ -463,14 +486,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (!ok) continue;
         // a tile of V that the producer mends first, once per tile
         if ((!wide || s == 0) && mends(ti)) {
-          ok = __all_sync(0xffffffffu, pa_wait(p, &mended[nmend % kXMend], (nmend / kXMend) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&mended[nmend % kXMend], (nmend / kXMend) & 1));
           ++nmend;
           if (!ok) continue;
         }
         const uint32_t b = desc_lo(ring + sl * L::kTile, 16384);
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
-          ok = ok && __all_sync(0xffffffffu, pa_wait(p, &p_full[2 * s + part], i & 1));
+          ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(&p_full[2 * s + part], i & 1));
           if (!ok) break;
           tc::fence_after_sync();
 #pragma unroll
@@ -509,12 +532,12 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float scale = rsqrtf((float)D) * kPaLog2e;
     const int pos = u.first_pos + (row >> p.g_shift);
-    const int ns = steps(s);
+    bool ok = !p.give_up;
+    const int ns = ok ? steps(s) : 0;
     float m = -INFINITY, l = 0.f;
-    bool ok = true;
     for (int i = 0; i < ns; ++i) {
       const int ti = tile_at(s, i), t = u.tile0 + ti;
-      ok = pa_wait(p, &mask_full[ti % kXMasks], (ti / kXMasks) & 1) && pa_wait(p, &s_full[s], i & 1);
+      ok = mbar_wait_bounded(&mask_full[ti % kXMasks], (ti / kXMasks) & 1) && mbar_wait_bounded(&s_full[s], i & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();
@@ -600,7 +623,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[2 * s + 1]);
     }
-    if (ok && ns > 0) ok = __all_sync(0xffffffffu, pa_wait(p, &o_done[s], 0));
+    if (ok && ns > 0) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&o_done[s], 0));
     if (!ok) s_abort = 1;
     tc::fence_after_sync();
     // O to memory through shared memory, so that a warp writes whole rows (a thread writing its own
@@ -686,20 +709,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (s_abort) {
-    if (tid == 0) report_timeout(g.status, 5);
-    // what the softmax warps wrote came from tiles that may not have been there
-    for (int r = tid; r < u.nrows; r += kXThreads) {
-      const long long id = row_id(r);
-      if (!g.direct) {
-        p.part_ml[u.slot * rows + id] = make_float2(0.f, NAN);
-        continue;
-      }
-      if (p.lse) p.lse[id] = NAN;
-      for (int c = 0; c < D; ++c)
-        static_cast<__nv_bfloat16*>(p.o)[id * D + c] = __float2bfloat16_rn(NAN);
-    }
-  }
+  if (s_abort) give_up<D>(p, g);
   if (warp == 9) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, 512);

@@ -661,10 +661,10 @@ bsa_status bsa_workspace_status(void* workspace, void* stream);
  * BSA_ERR_TIMEOUT; the CUDA context stays usable. */
 bsa_status bsa_selftest_bounded_wait(void* workspace, int polls, void* stream);
 
-/* Failure-path self-test of bsa_prefix_attn: in the following calls of this host thread a wait
- * between the roles of a CTA is given up after `polls` tries (0: at once), below 0: after the usual
- * number again.  Copies in flight are waited for as usual, so that the kernels end cleanly. */
-bsa_status bsa_selftest_prefix_waits(int polls);
+/* Failure-path self-test of bsa_prefix_attn: from now on (`on` nonzero) or no longer, in the calls
+ * of this host thread, the roles of a CTA act as if the first wait of each had run out.  Copies in
+ * flight are waited for as usual, so that the kernels end cleanly. */
+bsa_status bsa_selftest_prefix_timeout(int on);
 
 #ifdef __cplusplus
 }

@@ -237,9 +237,9 @@ WAITS = [
 
 @pytest.fixture
 def no_waiting(bsa_lib):
-    """Waits between the roles of a CTA run out at once."""
-    yield lambda: bsa_lib.bsa_selftest_prefix_waits(0)
-    bsa_lib.bsa_selftest_prefix_waits(-1)
+    """The first wait of each role of a CTA runs out."""
+    yield lambda: bsa_lib.bsa_selftest_prefix_timeout(1)
+    bsa_lib.bsa_selftest_prefix_timeout(0)
 
 
 @pytest.mark.parametrize("dtype,d,heads,kv_heads,page,prefix,B,most,own,launched", WAITS)
@@ -258,7 +258,7 @@ def test_waits_that_run_out(no_waiting, bsa_lib, dtype, d, heads, kv_heads, page
     assert int(status) == 0
     no_waiting()
     lost, lost_lse = m.run(ws=ws, status=status)
-    bsa_lib.bsa_selftest_prefix_waits(-1)
+    bsa_lib.bsa_selftest_prefix_timeout(0)
     assert int(status) != 0 and torch.isnan(lost).all() and torch.isnan(lost_lse).all()
     status.zero_()
     for _ in range(2):

@@ -172,9 +172,11 @@ __global__ void __launch_bounds__(kRThreads, 2)
   __shared__ long long s_run[2];  // the CTA's tiles
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  // Behind the tensor-core kernel the inputs are already there (it has waited for them before it
-  // let this one start); its own results are only the merge's concern, which waits for this kernel.
-  if (!g.after_tc) pdl_wait();
+  // Behind the tensor-core kernel the inputs are already there: it has waited for them before it
+  // let this one start.  The fence is so that this SM's L1 holds nothing older than that.  Its own
+  // results are only the merge's concern, which waits for this kernel.
+  if (g.after_tc) __threadfence();
+  else pdl_wait();
   pdl_trigger();
 
   // tiles of all requests, a run of consecutive requests per thread

@@ -17,9 +17,11 @@
 // requests for itself (one load and a scan are cheaper than a second launch or a grid-wide
 // exchange) and then handles its share of the requests' pages and of the tokens.  The cluster
 // barrier between reading lens / free and writing lens_out / free_out lets the caller pass the same
-// arrays (a state advanced in place). Measured: 5.2 us for a tick of 64 requests, of which 4 are
-// the launch and two dependent loads; 14 us for 1024 requests with a quarter million new tokens
-// (2.3 MB), whose instructions 8 to 16 SMs issue.
+// arrays (a state advanced in place). Measured: 5.3 us for a tick of 64 requests, of which 4 are
+// the launch and two dependent loads; 14.7 us for 1024 requests with a quarter million new tokens
+// (2.3 MB), whose instructions 16 SMs issue.  (With outputs that are none of the inputs nothing needs
+// the barrier: what is read behind it -- table entries that stay or leave, ring places head .. head +
+// taken -- is disjoint from what is written.  A grid over all SMs could then do such a step.)
 //
 // paged_append_kernel.  A copy bound by HBM: one 16-byte chunk of K and of V per thread and step,
 // neighbouring threads on neighbouring chunks of a head's row (256 B at d = 128 bf16), so reads
@@ -203,8 +205,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) page_tables_kernel(const PageTa
   }
 
   // slots and positions of the new tokens: a run of consecutive tokens per warp, 128 at a time,
-  // four a lane (with one a lane the 8 SMs spent 14 us issuing the instructions of a quarter
-  // million)
+  // four a lane: they share the search for their request and, as a rule, the page id, and issuing
+  // instructions is what a large step takes its time for
   const int gwarp = rank * warps + warp, gwarps = ranks * warps;
   const int total = s_cu[p.B];
   const long long run = (((long long)p.max_tokens + gwarps - 1) / gwarps + 127) / 128 * 128;
@@ -357,8 +359,9 @@ extern "C" bsa_status bsa_page_tables(int B, int page, const int* lens, const in
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   const long long work = (long long)B + max_tokens;
-  // 16 CTAs want to be two to an SM: with 8 a quarter million tokens took 20 us, with 16 14 us
-  const unsigned ctas = work <= kPtOneCta ? 1u : smem <= 100 * 1024 ? kPtCluster : kPtCluster / 2;
+  // One CTA to an SM (48 registers a thread).  With 8 CTAs 264K tokens of 1024 requests took 20.0 us,
+  // with 16 14.7; 2.2M tokens of 8192 requests 111 and 67 us.
+  const unsigned ctas = work <= kPtOneCta ? 1u : kPtCluster;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;

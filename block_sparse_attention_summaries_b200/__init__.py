@@ -890,11 +890,14 @@ def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q
         raise ValueError("ws must be uint8")
     else:
         _on_device(dev, ws)
-    _on_device(dev, k_pages, v_pages, table, lens, prefix_table, cu_q, status, slots)
-    _ints(table, lens, prefix_table, cu_q, status, slots)
-    num_slots = 0 if slots is None else slots.numel()
-    # an empty tensor has no address, but it is one: no token has a slot
-    at = None if slots is None else slots.data_ptr() or lens.data_ptr()
+    _on_device(dev, k_pages, v_pages, table, lens, prefix_table, cu_q, status)
+    _ints(table, lens, prefix_table, cu_q, status)
+    at, num_slots = None, 0
+    if slots is not None:
+        _on_device(dev, slots)
+        _ints(slots)
+        # an empty tensor has no address, but it is one: no token has a slot
+        at, num_slots = slots.data_ptr() or lens.data_ptr(), slots.numel()
     _call(lib().bsa_prefix_attn_slots, dev, "bsa_prefix_attn", q.data_ptr(), q_stride,
           k_pages.data_ptr(), v_pages.data_ptr(), dt, T, B, Hq, Hk, d, page, P, table.data_ptr(),
           table_ld, lens.data_ptr(), None if prefix_table is None else prefix_table.data_ptr(),

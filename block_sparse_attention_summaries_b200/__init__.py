@@ -121,12 +121,16 @@ def _stream(device=None):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+def _code_of(dtype: torch.dtype) -> int:
+    if dtype == torch.bfloat16:
         return BSA_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return BSA_F32
-    raise ValueError(f"unsupported dtype {t.dtype}")
+    raise ValueError(f"unsupported dtype {dtype}")
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return _code_of(t.dtype)
 
 
 def _cuda(*ts):
@@ -829,8 +833,7 @@ def prefix_attn_workspace_bytes(dtype, T, B, Hq, Hk, d, page, table_ld, prefix_l
                                 max_q=1) -> int:
     """Workspace bytes of prefix_attn for these sizes (max_q: T for a call with cu_q and no
     max_q)."""
-    dt = BSA_BF16 if dtype == torch.bfloat16 else BSA_F32
-    return _prefix_attn_bytes(dt, T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q)
+    return _prefix_attn_bytes(_code_of(dtype), T, B, Hq, Hk, d, page, table_ld, prefix_len, max_q)
 
 
 def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q=None, max_q=None,

@@ -359,7 +359,7 @@ extern "C" bsa_status bsa_page_tables(int B, int page, const int* lens, const in
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   const long long work = (long long)B + max_tokens;
-  // One CTA to an SM (48 registers a thread).  With 8 CTAs 264K tokens of 1024 requests took 20.0 us,
+  // One CTA to an SM (48 registers a thread).  With 8 CTAs 263K tokens of 1024 requests took 20.0 us,
   // with 16 14.7; 2.2M tokens of 8192 requests 111 and 67 us.
   const unsigned ctas = work <= kPtOneCta ? 1u : kPtCluster;
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -362,7 +362,9 @@ int pieces_for(long long units, long long ctas, long long tiles, int least) {
 constexpr int kRowsCtas = 2 * kSMs;  // of the few-rows kernel: two per SM
 constexpr int kRowsMax = 64;         // its rows
 // Key tiles of a kv head up to which a call is small: of the few-rows kernel, of the CUDA cores (a
-// tile takes those 2 us: with up to 8 a CTA 10 requests of 500 keys took 57 us instead of 45)
+// tile takes those 2 us: with up to 8 a CTA 10 requests of 500 keys took 57 us instead of 45; with up
+// to 2 a call from Python takes 24.4 us instead of 26.2 (4 requests behind 500), while the device,
+// which the host keeps waiting, is at it for 16.6 us instead of 12.3)
 constexpr long long kClusterTiles = 4 * kClusterCtas, kClusterTiles2 = 2 * kClusterCtas;
 // Key tiles of 32 KB (over all heads and row groups) up to which the few-rows kernel takes the
 // prefix of more rows: four a CTA.
@@ -420,8 +422,9 @@ PrefixPlan plan_of(bsa_dtype dt, int T, int B, int Hq, int Hk, int d, int page, 
     w.prefix_rows = 16 * w.mt;
     w.own_rows = (int)rows_q;
     w.items = ((long long)w.groups + B) * Hk;
-    // A small call is one launch: a cluster per kv head (4 requests behind 1000 tokens: 11.5 us as
-    // two). With fewer CTAs than the GPU holds it loses that again once each has several tiles.
+    // A small call is one launch: a cluster per kv head (4 requests behind 1000 tokens: 11.3 us on
+    // the device and 24.5 us a call from Python, as two launches 11.7 and 26.2). With fewer CTAs
+    // than the GPU holds it loses that again once each has several tiles.
     w.cluster = !w.tc1 && (long long)w.groups * tiles(prefix_len, 8192 / d) +
                                   (long long)B * tiles(keys2, 8192 / d) <= kClusterTiles;
     w.item_ctas = w.cluster ? kClusterCtas : kRowsCtas;

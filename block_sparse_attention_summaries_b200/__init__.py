@@ -766,9 +766,8 @@ def page_tables(lens, new_lens, table, ring, free, page, max_tokens, pos_offset=
     request goes from lens to new_lens tokens; ``table`` and ``ring`` are updated in place.
     ``status`` (int32 [1], optional) collects PAGES_* bits.  Tokens of a request that finds no pages,
     and those past max_tokens, have slot -1: pass the slots on to paged_append and prefix_attn.
-    Returns (lens_out [B], free_out [2],
-    cu_new [B + 1], slots [max_tokens], positions [max_tokens]); pass lens_out=lens and
-    free_out=free to advance the state in place."""
+    Returns (lens_out [B], free_out [2], cu_new [B + 1], slots [max_tokens], positions
+    [max_tokens]); pass lens_out=lens and free_out=free to advance the state in place."""
     dev = _device_index(lens)
     B = lens.numel()
     shape = table.shape
@@ -849,9 +848,9 @@ def prefix_attn(q, k_pages, v_pages, table, lens, prefix_table, prefix_len, cu_q
     tokens before the first or beyond max_q) are left as they were: undefined in an o and lse
     allocated here.  ``slots`` (int32, optional): the step's slots as page_tables returned them; a
     token without one (its request was refused, or max_tokens was too small) gets o = 0, lse = -inf
-    instead of passing for its request's last token.  ``ws``: a uint8 device tensor of at least prefix_attn_workspace_bytes bytes
-    (allocated here when None).  ``status`` (int32 [1], optional): set nonzero if a bounded device
-    wait ran out.  Returns (o, lse)."""
+    instead of passing for its request's last token.  ``ws``: a uint8 device tensor of at least
+    prefix_attn_workspace_bytes bytes (allocated here when None).  ``status`` (int32 [1], optional):
+    set nonzero if a bounded device wait ran out; the rows concerned are NaN.  Returns (o, lse)."""
     shape, q_stride = _heads(q, "q")
     T, Hq, d = shape
     pool = k_pages.shape

@@ -248,8 +248,7 @@ __device__ __noinline__ void give_up(const PrefixParams& p, const TcGrid& g) {
   if (threadIdx.x == 0) report_timeout(g.status, 5);
   for (int r = threadIdx.x; r < u.nrows; r += kXThreads) {
     const int rr = u.r0 + r;
-    const long long id =
-        (long long)(rr >> p.g_shift) * p.Hq + u.h * p.G + (rr & (p.G - 1));
+    const long long id = (long long)(rr >> p.g_shift) * p.Hq + u.h * p.G + (rr & (p.G - 1));
     if (!g.direct) {
       p.part_ml[(long long)u.slot * p.T * p.Hq + id] = make_float2(0.f, NAN);
       continue;
@@ -486,7 +485,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (!ok) continue;
         // a tile of V that the producer mends first, once per tile
         if ((!wide || s == 0) && mends(ti)) {
-          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&mended[nmend % kXMend], (nmend / kXMend) & 1));
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&mended[nmend % kXMend],
+                                                         (nmend / kXMend) & 1));
           ++nmend;
           if (!ok) continue;
         }
@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
     float m = -INFINITY, l = 0.f;
     for (int i = 0; i < ns; ++i) {
       const int ti = tile_at(s, i), t = u.tile0 + ti;
-      ok = mbar_wait_bounded(&mask_full[ti % kXMasks], (ti / kXMasks) & 1) && mbar_wait_bounded(&s_full[s], i & 1);
+      ok = mbar_wait_bounded(&mask_full[ti % kXMasks], (ti / kXMasks) & 1) &&
+           mbar_wait_bounded(&s_full[s], i & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc::fence_after_sync();

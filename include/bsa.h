@@ -542,8 +542,8 @@ typedef enum {
  * none: both are tokens of the step without a slot.  bsa_paged_append skips them, and
  * bsa_prefix_attn_slots answers them with o = 0 and lse = -inf.  (bsa_prefix_attn, which is not told,
  * would take those of a refused request for its last tokens.)  Past max_tokens lens_out counts the
- * tokens all the same, and their pages are theirs: a caller that sees BSA_PAGES_TOKENS writes
- * their keys and values, or goes back to the lengths before, before a later step attends to them.
+ * tokens all the same, and their pages are theirs, but their keys and values are not in the cache: a
+ * caller that sees BSA_PAGES_TOKENS writes them, or returns to the old lengths, before the next step.
  * Limits: B <= 8192, num_pages * page < 2^31.  Deterministic; one launch.
  */
 bsa_status bsa_page_tables(int B, int page, const int* lens, const int* new_lens, int* table,
@@ -580,8 +580,8 @@ bsa_status bsa_paged_append(const void* k, const void* v, bsa_dtype dt, int T, i
  *   o [T, Hq, d] out; lse [T, Hq] optional out.  A token that sees no key gets o = 0, lse = -inf.
  *             Rows at or after cu_q[B], and tokens beyond the max_q-th of a request, are left as
  *             they were.
- *   status    optional device int: a bounded wait that runs out writes a nonzero value there; o
- *             and lse are then not valid.
+ *   status    optional device int: a bounded wait that runs out writes a nonzero value there; the
+ *             rows concerned are then NaN in o and lse.
  *   workspace device scratch of bsa_prefix_attn_workspace_bytes() bytes, 16-byte aligned; needs no
  *             initialisation and may be reused once the stream has passed the call.  Calls that
  *             share one must not run at the same time.
